@@ -17,7 +17,9 @@
  * computed in fp32 on the device and rounded to the element type with
  * round-to-nearest-even.  Variants of the output (the "epilogues": a weight
  * offset, MXFP8 / MXFP4 / NVFP4 block-scaled codes) and the per-head QK norm
- * are declared further down, each with its own definition.
+ * are declared further down, each with its own definition.  rmsnorm_rope.h
+ * declares the QK norm with the position rotation, the same with keys and
+ * values appended to a paged cache, and the gradients of these norms.
  *
  * Memory layout.  x and y are row-major [rows, hidden], contiguous (row
  * stride = hidden elements); weight is [hidden].  x, weight and y share one
@@ -72,6 +74,7 @@ typedef enum {
     RMSNORM_ERR_UNSUPPORTED_DEVICE = 8, /* current device is not compute capability 10.3 */
     RMSNORM_ERR_VARIANT = 9,            /* forced variant cannot take this shape */
     RMSNORM_ERR_TOO_LARGE = 10          /* beyond the static scratch of rmsnorm_fwd_staged_noalloc */
+    /* 11: RMSNORM_ERR_BAD_INDEX (rmsnorm_rope.h) */
 } rmsnorm_status_t;
 
 /* What a row kernel writes (see rmsnorm_fwd_bias and rmsnorm_fwd_mxfp8). */

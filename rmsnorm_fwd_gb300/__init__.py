@@ -33,6 +33,7 @@ ERR_MISALIGNED = 7
 ERR_UNSUPPORTED_DEVICE = 8
 ERR_VARIANT = 9
 ERR_TOO_LARGE = 10
+ERR_BAD_INDEX = 11
 
 # variants (rmsnorm_variant_t)
 VARIANT_AUTO = 0
@@ -90,6 +91,28 @@ class KernelInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class Heads(ctypes.Structure):
+    """rmsnorm_heads_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """rmsnorm_rope_t."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("max_position", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class PagedCache(ctypes.Structure):
+    """rmsnorm_paged_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("e4m3", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -112,6 +135,8 @@ def _load() -> ctypes.CDLL:
         vp, i64, i32, f32, u64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                                   ctypes.c_uint64)
         pp = ctypes.POINTER(Plan)
+        hp, rp, szp = (ctypes.POINTER(Heads), ctypes.POINTER(Rope),
+                       ctypes.POINTER(ctypes.c_size_t))
         sig = {
             "rmsnorm_create": ([], i32),
             "rmsnorm_destroy": ([], i32),
@@ -134,6 +159,18 @@ def _load() -> ctypes.CDLL:
             "rmsnorm_plan_epilogue": ([vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, pp], i32),
             "rmsnorm_validate_plan_epilogue": ([pp, vp, vp, vp, i64, i64, i32, i32, i32, i32],
                                                i32),
+            "rmsnorm_qk_norm_rope": ([hp, hp, hp, hp, vp, vp, rp, i64, i64, i64, i64, f32, f32,
+                                      i32, vp], i32),
+            "rmsnorm_qk_norm_rope_bwd": ([hp, hp, hp, hp, hp, hp, vp, vp, vp, vp, rp, vp,
+                                          ctypes.c_size_t, i64, i64, i64, i64, f32, f32, i32,
+                                          vp], i32),
+            "rmsnorm_qk_norm_rope_bwd_workspace": ([i64, i32, szp], i32),
+            "rmsnorm_qk_norm_rope_append": ([hp, hp, hp, hp, vp, vp, rp,
+                                             ctypes.POINTER(PagedCache), vp, i64, i64, i64, i64,
+                                             f32, f32, i32, vp], i32),
+            "rmsnorm_bwd": ([vp, vp, vp, vp, vp, vp, ctypes.c_size_t, i64, i64, f32, f32, i32,
+                             vp], i32),
+            "rmsnorm_bwd_workspace": ([i64, i64, i32, i32, szp], i32),
             "rmsnorm_last_variant": ([], i32),
             "rmsnorm_kernel_count": ([], i32),
             "rmsnorm_validate_plan": ([pp, vp, vp, vp, i64, i64, i32, i32, i32], i32),
@@ -296,6 +333,65 @@ def rmsnorm_validate_plan_epilogue(plan: Plan, x: int, weight: int, y: int, rows
                                    smem_optin: int) -> int:
     return _load().rmsnorm_validate_plan_epilogue(ctypes.byref(plan), x, weight, y, rows, hidden,
                                                   dtype, epilogue, sm_count, smem_optin)
+
+
+def rmsnorm_qk_norm_rope(q: Heads | None, k: Heads | None, q_out: Heads | None,
+                         k_out: Heads | None, q_weight: int, k_weight: int, rope: Rope,
+                         tokens: int, q_heads: int, k_heads: int, head_dim: int,
+                         weight_bias: float, eps: float, dtype: int,
+                         stream: int | None) -> None:
+    """Per-head QK norm and position rotation (structures with device pointers)."""
+    _check(_load().rmsnorm_qk_norm_rope(q, k, q_out, k_out, q_weight or None, k_weight or None,
+                                        rope, tokens, q_heads, k_heads, head_dim, weight_bias,
+                                        eps, dtype, stream or None), "rmsnorm_qk_norm_rope")
+
+
+def rmsnorm_qk_norm_rope_bwd(dq_out: Heads | None, dk_out: Heads | None, q: Heads | None,
+                             k: Heads | None, dq: Heads | None, dk: Heads | None, q_weight: int,
+                             k_weight: int, dq_weight: int, dk_weight: int, rope: Rope,
+                             workspace: int, workspace_bytes: int, tokens: int, q_heads: int,
+                             k_heads: int, head_dim: int, weight_bias: float, eps: float,
+                             dtype: int, stream: int | None) -> None:
+    _check(_load().rmsnorm_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, q_weight or None,
+                                            k_weight or None, dq_weight or None,
+                                            dk_weight or None, rope, workspace or None,
+                                            workspace_bytes, tokens, q_heads, k_heads, head_dim,
+                                            weight_bias, eps, dtype, stream or None),
+           "rmsnorm_qk_norm_rope_bwd")
+
+
+def rmsnorm_qk_norm_rope_bwd_workspace(head_dim: int, sm_count: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_load().rmsnorm_qk_norm_rope_bwd_workspace(head_dim, sm_count, ctypes.byref(n)),
+           "rmsnorm_qk_norm_rope_bwd_workspace")
+    return n.value
+
+
+def rmsnorm_qk_norm_rope_append(q: Heads | None, k: Heads, v: Heads, q_out: Heads | None,
+                                q_weight: int, k_weight: int, rope: Rope, cache: PagedCache,
+                                slots: int, tokens: int, q_heads: int, k_heads: int,
+                                head_dim: int, weight_bias: float, eps: float, dtype: int,
+                                stream: int | None) -> None:
+    _check(_load().rmsnorm_qk_norm_rope_append(q, k, v, q_out, q_weight or None,
+                                               k_weight or None, rope, cache, slots or None,
+                                               tokens, q_heads, k_heads, head_dim, weight_bias,
+                                               eps, dtype, stream or None),
+           "rmsnorm_qk_norm_rope_append")
+
+
+def rmsnorm_bwd(dy: int, x: int, weight: int, dx: int, dweight: int, workspace: int,
+                workspace_bytes: int, rows: int, hidden: int, weight_bias: float, eps: float,
+                dtype: int, stream: int | None) -> None:
+    _check(_load().rmsnorm_bwd(dy or None, x or None, weight or None, dx or None,
+                               dweight or None, workspace or None, workspace_bytes, rows, hidden,
+                               weight_bias, eps, dtype, stream or None), "rmsnorm_bwd")
+
+
+def rmsnorm_bwd_workspace(rows: int, hidden: int, dtype: int, sm_count: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_load().rmsnorm_bwd_workspace(rows, hidden, dtype, sm_count, ctypes.byref(n)),
+           "rmsnorm_bwd_workspace")
+    return n.value
 
 
 def rmsnorm_plan(x: int, weight: int, y: int, rows: int, hidden: int, dtype: int, sm_count: int,
@@ -546,3 +642,246 @@ def _check_rows(x, weight):
         raise ValueError("x and weight must be contiguous")
     if weight.numel() != x.shape[-1]:
         raise ValueError("weight must have hidden elements")
+
+
+def _launch_on(device, stream, call):
+    """call(raw stream) with `device` current, on `stream` or the device's
+    current stream.  Tensors made in `call` belong to that stream."""
+    import torch
+    ensure_context(device.index)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _heads_of(t, name: str, like=None):
+    """(rmsnorm_heads_t, tokens) of a CUDA tensor [..., heads, head_dim] whose
+    leading dimensions step evenly over the tokens."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3:
+        raise ValueError(f"{name} must be [..., tokens, heads, head_dim]")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} must have the dtype and device of the other tensors")
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    tokens, step = 1, 0
+    for n, s in zip(shape[-3::-1], strides[-3::-1]):
+        if n != 1:
+            if tokens == 1:
+                step = s
+            elif s != step * tokens:
+                raise ValueError(f"the leading dimensions of {name} must step evenly")
+            tokens *= n
+    heads = shape[-2]
+    if t.numel() and ((tokens > 1 and step == 0) or (heads > 1 and strides[-2] == 0)):
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return Heads(t.data_ptr(), step, strides[-2] if heads > 1 else 0), tokens
+
+
+def _rope_of(cos_sin, positions, tokens: int, interleaved: bool, device) -> Rope:
+    import torch
+    if cos_sin is None:
+        return Rope(None, None, 0, 0, 0)
+    if cos_sin.dtype != torch.float32 or positions.dtype != torch.int64:
+        raise TypeError("cos_sin must be float32 and positions int64")
+    if cos_sin.device != device or positions.device != device:
+        raise ValueError("cos_sin and positions must be on the device of q and k")
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or not positions.is_contiguous():
+        raise ValueError("cos_sin must be [max_position, rotary_dim], cos_sin and positions "
+                         "contiguous")
+    if positions.numel() != tokens:
+        raise ValueError("positions must hold one position for each token")
+    return Rope(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                1 if interleaved else 0)
+
+
+def _head_weight(w, name: str, like) -> int:
+    if w is None:
+        return 0
+    if w.dtype != like.dtype or w.device != like.device:
+        raise TypeError(f"{name} must have the dtype and device of its heads")
+    if w.numel() != like.shape[-1] or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, with head_dim elements")
+    return w.data_ptr()
+
+
+def _same_shape(t, like, name: str) -> None:
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have the shape of its input")
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
+                 weight_bias: float = 0.0, interleaved: bool = False, q_out=None, k_out=None,
+                 stream=None):
+    """Per-head norm and position rotation of q [..., q_heads, head_dim] and k
+    [..., k_heads, head_dim] in one pass (rmsnorm_qk_norm_rope): in place, or
+    into q_out / k_out.  Returns (q_out, k_out).
+
+    Every tensor's leading dimensions are the tokens and must step evenly;
+    heads may be strided (views into a fused QKV tensor, head-major layouts).
+    ``cos_sin``: float32 [max_position, rotary_dim], a row holding the cosines
+    of a position's rotary_dim / 2 angles and then their sines; ``positions``:
+    int64, one for each token; both None: no rotation.  ``k`` may be None.
+    A position outside the table leaves its token out and is reported by
+    rmsnorm_get_device_status (ERR_BAD_INDEX).  Runs on ``stream`` (default:
+    PyTorch's current stream)."""
+    qh, tokens = _heads_of(q, "q")
+    kh, k_tokens = (None, tokens) if k is None else _heads_of(k, "k", q)
+    if k_tokens != tokens or (k is not None and k.shape[-1] != q.shape[-1]):
+        raise ValueError("q and k must hold the same number of tokens and one head_dim")
+    qo = ko = None
+    if q_out is not None:
+        _same_shape(q_out, q, "q_out")
+        qo = _heads_of(q_out, "q_out", q)[0]
+    if k_out is not None:
+        _same_shape(k_out, k, "k_out")
+        ko = _heads_of(k_out, "k_out", q)[0]
+    rope = _rope_of(cos_sin, positions, tokens, interleaved, q.device)
+    qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
+    k_heads = 0 if k is None else k.shape[-2]
+    _launch_on(q.device, stream, lambda s: rmsnorm_qk_norm_rope(
+        qh, kh, qo, ko, qw, kw, rope, tokens, q.shape[-2], k_heads, q.shape[-1], weight_bias, eps,
+        torch_dtype_code(q.dtype), s))
+    return q if q_out is None else q_out, k if k_out is None else k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions,
+                          eps: float, weight_bias: float = 0.0, interleaved: bool = False,
+                          dq=None, dk=None, weight_grads: bool = True, stream=None):
+    """Gradient of ``qk_norm_rope`` (rmsnorm_qk_norm_rope_bwd): (dq, dk,
+    dq_weight, dk_weight) from the gradients of its outputs and its inputs q
+    and k as they were before the call (so that call must not be in place).
+    dq / dk: optional outputs, which may be dq_out / dk_out or q / k
+    themselves; by default new contiguous tensors.  The weights' gradients are
+    float32 [head_dim] (None with ``weight_grads=False``).  k and dk_out may
+    be None.  Other arguments as for ``qk_norm_rope``."""
+    import torch
+    qh, tokens = _heads_of(q, "q")
+    kh, k_tokens = (None, tokens) if k is None else _heads_of(k, "k", q)
+    if k_tokens != tokens or (k is not None and k.shape[-1] != q.shape[-1]):
+        raise ValueError("q and k must hold the same number of tokens and one head_dim")
+    _same_shape(dq_out, q, "dq_out")
+    qy, ky = _heads_of(dq_out, "dq_out", q)[0], None
+    if k is not None:
+        _same_shape(dk_out, k, "dk_out")
+        ky = _heads_of(dk_out, "dk_out", q)[0]
+    rope = _rope_of(cos_sin, positions, tokens, interleaved, q.device)
+    qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
+    head_dim, k_heads = q.shape[-1], 0 if k is None else k.shape[-2]
+
+    def call(s):
+        q_grad = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        _same_shape(q_grad, q, "dq")
+        k_grad = dk
+        if k is not None:
+            if k_grad is None:
+                k_grad = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            _same_shape(k_grad, k, "dk")
+        w_grads = ws = None
+        if weight_grads:
+            need = rmsnorm_qk_norm_rope_bwd_workspace(head_dim, rmsnorm_device_limits()[0])
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            w_grads = torch.empty(2, head_dim, dtype=torch.float32, device=q.device)
+        p = w_grads.data_ptr() if weight_grads else 0
+        rmsnorm_qk_norm_rope_bwd(qy, ky, qh, kh, _heads_of(q_grad, "dq", q)[0],
+                                 None if k is None else _heads_of(k_grad, "dk", q)[0], qw, kw, p,
+                                 p + 4 * head_dim if p else 0, rope, ws.data_ptr() if p else 0,
+                                 ws.numel() if p else 0, tokens, q.shape[-2], k_heads, head_dim,
+                                 weight_bias, eps, torch_dtype_code(q.dtype), s)
+        if not weight_grads:
+            return q_grad, k_grad, None, None
+        return q_grad, k_grad, w_grads[0], w_grads[1]
+
+    return _launch_on(q.device, stream, call)
+
+
+def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, k_cache, v_cache,
+                        eps: float, weight_bias: float = 0.0, interleaved: bool = False,
+                        k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, stream=None):
+    """``qk_norm_rope`` with the keys and values appended to a paged cache in
+    the same launch (rmsnorm_qk_norm_rope_append): q in place or into q_out, k
+    and v into k_cache and v_cache [pages, page_size, k_heads, head_dim] (any
+    strides but the last; head-first caches come as transposed views) at
+    slots[t] = page * page_size + slot.  Returns q_out.
+
+    ``slots``: int64, one for each token; a negative one marks padding, of
+    which nothing is read or written; the others must differ.  Caches hold the
+    elements' dtype, or E4M3 codes of value / scale (float8_e4m3fn or uint8).
+    Weights None: the rotation alone.  k and v are left as they were; ``q`` may
+    be None."""
+    import torch
+    kh, tokens = _heads_of(k, "k")
+    vh, v_tokens = _heads_of(v, "v", k)
+    qh, q_tokens = (None, tokens) if q is None else _heads_of(q, "q", k)
+    if v.shape[-2:] != k.shape[-2:] or v_tokens != tokens or q_tokens != tokens or \
+            (q is not None and q.shape[-1] != k.shape[-1]):
+        raise ValueError("q, k and v must hold the same number of tokens and one head_dim, k and "
+                         "v the same heads")
+    qo = None
+    if q_out is not None:
+        _same_shape(q_out, q, "q_out")
+        qo = _heads_of(q_out, "q_out", k)[0]
+    if slots.dtype != torch.int64:
+        raise TypeError("slots must be int64")
+    if slots.device != k.device or slots.numel() != tokens or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous, one for each token, on the device of k")
+    k_heads, head_dim = k.shape[-2], k.shape[-1]
+    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[-2:] or \
+            v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, head_dim] with "
+                         "the same strides")
+    if k_cache.dtype != v_cache.dtype or k_cache.device != k.device or v_cache.device != k.device:
+        raise TypeError("k_cache and v_cache must have one dtype and the device of k")
+    st = k_cache.stride()
+    if head_dim > 1 and st[3] != 1:
+        raise ValueError("the last dimension of the caches must be contiguous")
+    e4m3 = k_cache.dtype in (torch.float8_e4m3fn, torch.uint8)
+    if not e4m3 and k_cache.dtype != k.dtype:
+        raise TypeError("the caches must hold the dtype of k, float8_e4m3fn or uint8")
+    cache = PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1],
+                       st[0], st[1], st[2], 1 if e4m3 else 0, k_scale, v_scale)
+    rope = _rope_of(cos_sin, positions, tokens, interleaved, k.device)
+    qw, kw = _head_weight(q_weight, "q_weight", k), _head_weight(k_weight, "k_weight", k)
+    q_heads = 0 if q is None else q.shape[-2]
+    _launch_on(k.device, stream, lambda s: rmsnorm_qk_norm_rope_append(
+        qh, kh, vh, qo, qw, kw, rope, cache, slots.data_ptr(), tokens, q_heads, k_heads, head_dim,
+        weight_bias, eps, torch_dtype_code(k.dtype), s))
+    return q if q_out is None else q_out
+
+
+def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=None,
+                      weight_grad: bool = True, stream=None):
+    """Gradient of ``rms_norm`` (of ``rms_norm_bias`` with ``weight_bias``)
+    through rmsnorm_bwd: (dx, dweight) from dy, the gradient of the output, and
+    x, the input.  Tensors as for ``rms_norm``; ``dx``: optional output, which
+    may be dy or x itself; dweight is float32 [hidden] (None with
+    ``weight_grad=False``)."""
+    import torch
+    _check_rows(x, weight)
+    for t, name in ((dy, "dy"), (dx, "dx")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or
+                              t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must match x (shape, dtype, device, contiguous)")
+    if weight.device != x.device:
+        raise ValueError("weight must be on the device of x")
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden if hidden else 0
+    code = torch_dtype_code(x.dtype)
+
+    def call(s):
+        grad = torch.empty_like(x) if dx is None else dx
+        need = rmsnorm_bwd_workspace(rows, hidden, code, rmsnorm_device_limits()[0])
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        w_grad = torch.empty(hidden, dtype=torch.float32, device=x.device) if weight_grad else None
+        rmsnorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), grad.data_ptr(),
+                    w_grad.data_ptr() if weight_grad else 0, ws.data_ptr(), need, rows, hidden,
+                    weight_bias, eps, code, s)
+        return grad, w_grad
+
+    return _launch_on(x.device, stream, call)

@@ -21,11 +21,12 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "librmsnorm.so")
 
 SOURCES = ["api.cpp", "select.cpp", "generic.cu", "staged.cu", "qknorm.cu", "cluster.cu",
-           "gridrow.cu",
+           "gridrow.cu", "api_rope.cpp", "rope.cu", "rope_bwd.cu", "rms_bwd.cu", "colsum.cu",
            "rowreg_f32.cu", "rowreg_bf16.cu", "rowreg_f16.cu",
            "rowreg_epi_f32.cu", "rowreg_epi_bf16.cu", "rowreg_epi_f16.cu",
            "rowreg_fp4_f32.cu", "rowreg_fp4_bf16.cu", "rowreg_fp4_f16.cu"]
-HEADERS = ["internal.h", "host_link.h", "device_common.cuh", "rowreg.cuh"]
+HEADERS = ["internal.h", "host_link.h", "strides.h", "device_common.cuh", "rowreg.cuh",
+           "rope_args.h", "rope.cuh"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC"]
 CUDA_FLAGS = ["-lineinfo"]
@@ -44,7 +45,7 @@ def _cuda_home(nvcc: str) -> str:
 
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    paths += [os.path.join(INCLUDE, "rmsnorm.h"), __file__]
+    paths += [os.path.join(INCLUDE, h) for h in ("rmsnorm.h", "rmsnorm_rope.h")] + [__file__]
     return max(os.path.getmtime(p) for p in paths)
 
 

@@ -14,6 +14,8 @@
 
 #include "host_link.h"
 #include "internal.h"
+#include "rope_args.h"
+#include "strides.h"
 
 namespace rmsnorm {
 
@@ -344,6 +346,19 @@ int launch(const void *x, const void *w, void *y, int64_t rows, int64_t hidden, 
 
 } // namespace
 
+int call_context(CallContext *out)
+{
+    DeviceCtx ctx;
+    const int rc = current_ctx(&ctx, nullptr);
+    if (rc != RMSNORM_OK)
+        return rc;
+    out->sm_count = ctx.sm_count;
+    out->smem_optin = ctx.smem_optin;
+    out->status = ctx.status;
+    out->pdl = pdl_enabled();
+    return RMSNORM_OK;
+}
+
 int check_call_args(const void *x, const void *w, const void *y, int64_t rows, int64_t hidden,
                     float eps, int dtype)
 {
@@ -501,48 +516,6 @@ int rmsnorm_fwd_epilogue_ex(const void *x, const void *weight, void *y, void *sc
                   epilogue == RMSNORM_EPI_PLAIN ? -0.0f : weight_bias,
                   epilogue >= RMSNORM_EPI_MXFP8 ? scales : nullptr,
                   epilogue == RMSNORM_EPI_NVFP4 ? global_scale : 1.0f);
-}
-
-// Whether two strided head sets can share a byte: set A is
-// {a + t * sa + [0, la)} and set B {b + t * sb + [0, lb)} for t < tokens (bytes).
-bool strided_overlap(uintptr_t a, int64_t sa, int64_t la, uintptr_t b, int64_t sb, int64_t lb,
-                     int64_t tokens)
-{
-    if (tokens <= 0 || la <= 0 || lb <= 0)
-        return false;
-    const int64_t ea = (tokens - 1) * sa + la, eb = (tokens - 1) * sb + lb;
-    if (!ranges_overlap(reinterpret_cast<const void *>(a), ea, reinterpret_cast<const void *>(b),
-                        eb))
-        return false; // the whole extents are apart
-    if (sa != sb || sa <= 0)
-        return true; // interleaved with different strides: refuse
-    // Equal strides P: some pair of tokens collides iff d + m P lies in
-    // (-lb, la) for an integer |m| < tokens, with d = b - a.
-    const int64_t d = static_cast<int64_t>(b - a), P = sa;
-    auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
-    int64_t m_lo = floor_div(-lb - d, P) + 1;           // smallest m with d + mP > -lb
-    int64_t m_hi = -floor_div(-(la - d), P) - 1;        // largest m with d + mP < la
-    m_lo = std::max(m_lo, -(tokens - 1));
-    m_hi = std::min(m_hi, tokens - 1);
-    return m_lo <= m_hi;
-}
-
-// Whether the interval [w, w + wb) meets {a + t * P + [0, la)}, t < tokens.
-bool interval_hits_strided(uintptr_t a, int64_t P, int64_t la, int64_t tokens, uintptr_t w,
-                           int64_t wb)
-{
-    if (tokens <= 0 || la <= 0 || wb <= 0)
-        return false;
-    const int64_t d = static_cast<int64_t>(w - a);
-    if (P <= 0) // a single interval
-        return d < la && -d < wb;
-    // t P < d + wb and d < t P + la, for an integer t in [0, tokens)
-    auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
-    int64_t t_lo = floor_div(d - la, P) + 1;   // smallest t with t P > d - la
-    int64_t t_hi = -floor_div(-(d + wb), P) - 1; // largest t with t P < d + wb
-    t_lo = std::max<int64_t>(t_lo, 0);
-    t_hi = std::min<int64_t>(t_hi, tokens - 1);
-    return t_lo <= t_hi;
 }
 
 int rmsnorm_fwd_host(const void *x_host, const void *weight, void *y_host, int64_t rows,
@@ -965,6 +938,8 @@ const char *rmsnorm_status_string(int status)
         return "the forced variant or plan cannot take this shape";
     case RMSNORM_ERR_TOO_LARGE:
         return "beyond the static scratch of the allocation-free entry point";
+    case RMSNORM_ERR_BAD_INDEX:
+        return "a position outside the rotation table or a slot outside the cache";
     default:
         return "unknown status";
     }
