@@ -42,8 +42,8 @@ typedef struct {
  * 2i with element 2i + 1:
  *   y_a = u_a cos_i - u_b sin_i,   y_b = u_b cos_i + u_a sin_i.
  * A position outside [0, max_position) is found on the device: the token is
- * left out (nothing of it is read or written, and it adds nothing to a
- * weight's gradient) and RMSNORM_ERR_BAD_INDEX is recorded in the device
+ * left out (nothing of it is written, and it adds nothing to a weight's
+ * gradient) and RMSNORM_ERR_BAD_INDEX is recorded in the device
  * status word (rmsnorm_get_device_status). */
 typedef struct {
     const float *cos_sin;
@@ -64,10 +64,9 @@ typedef struct {
  *                 interleave with different strides count as overlapping).
  *   q_weight, k_weight  DEVICE, [head_dim] of `dtype`; may be equal
  *   head_dim      1 .. 1024;  tokens >= 0;  weight_bias finite;  eps >= 0, finite
- * Heads that can be read in 16-byte vectors holding whole pairs (data,
- * weights and strides on 16-byte boundaries, and rotary_dim / 2 -- or, with
- * `interleaved`, rotary_dim -- and (head_dim - rotary_dim) filling whole
- * vectors, two for each lane) take the vector kernel, others a scalar one.
+ * Heads that can be read in vectors of 16, 8 or 4 bytes (data, weights,
+ * strides and the table on such boundaries, head_dim and rotary_dim multiples of
+ * two vectors' elements) take a vector kernel, others a scalar one.
  * Enqueues one kernel on `stream`; does not synchronise.  Returns RMSNORM_OK,
  * RMSNORM_ERR_INVALID_ARG, RMSNORM_ERR_UNSUPPORTED_DTYPE,
  * RMSNORM_ERR_ALIASING, RMSNORM_ERR_NOT_INITIALIZED or RMSNORM_ERR_CUDA. */
@@ -133,7 +132,7 @@ typedef struct {
  * type; k itself is left as it was), v is copied there (or rounded to E4M3).
  * Token t goes to slot slots[t] % page_size of page slots[t] / page_size
  * (DEVICE, int64).  A negative slot marks padding: nothing of the token is
- * read (its position neither) or written, its q_out row included.  A slot
+ * written, its q_out row included, and its values and position have no effect.  A slot
  * beyond the cache leaves the token out and records RMSNORM_ERR_BAD_INDEX, as
  * a position outside the table does.  The non-negative slots of one call must
  * differ: which of two tokens in one slot remains is not defined, byte by

@@ -811,7 +811,8 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
     slots[t] = page * page_size + slot.  Returns q_out.
 
     ``slots``: int64, one for each token; a negative one marks padding, of
-    which nothing is read or written; the others must differ.  Caches hold the
+    which nothing is written and whose values have no effect; the others must
+    differ.  Caches hold the
     elements' dtype, or E4M3 codes of value / scale (float8_e4m3fn or uint8).
     Weights None: the rotation alone.  k and v are left as they were; ``q`` may
     be None."""

@@ -21,12 +21,13 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "librmsnorm.so")
 
 SOURCES = ["api.cpp", "select.cpp", "generic.cu", "staged.cu", "qknorm.cu", "cluster.cu",
-           "gridrow.cu", "api_rope.cpp", "rope.cu", "rope_bwd.cu", "rms_bwd.cu", "colsum.cu",
+           "gridrow.cu", "api_rope.cpp", "rope.cu", "rope_f32.cu", "rope_bf16.cu", "rope_f16.cu",
+           "rope_bwd.cu", "rms_bwd.cu", "colsum.cu",
            "rowreg_f32.cu", "rowreg_bf16.cu", "rowreg_f16.cu",
            "rowreg_epi_f32.cu", "rowreg_epi_bf16.cu", "rowreg_epi_f16.cu",
            "rowreg_fp4_f32.cu", "rowreg_fp4_bf16.cu", "rowreg_fp4_f16.cu"]
 HEADERS = ["internal.h", "host_link.h", "strides.h", "device_common.cuh", "rowreg.cuh",
-           "rope_args.h", "rope.cuh"]
+           "rope_args.h", "rope.cuh", "ropevec.cuh"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC"]
 CUDA_FLAGS = ["-lineinfo"]

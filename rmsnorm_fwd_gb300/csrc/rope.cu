@@ -1,5 +1,6 @@
 // rope.cu -- per-head QK norm and position rotation in one pass, and the same
-// with keys and values appended to a paged cache.
+// with keys and values appended to a paged cache: the scalar body, and which
+// body takes a call.
 //
 //   u[d] = (x[d] * r) * (w[d] + bias),  r = rsqrt(mean x^2 + eps)
 //   y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin   for each rotated pair
@@ -117,6 +118,13 @@ template <int DT> cudaError_t launch_scalar(const RopeArgs &a)
 
 cudaError_t launch_rope(const RopeArgs &a, int dtype)
 {
+    const auto vec = dtype == RMSNORM_F32    ? launch_rope_vec_f32
+                     : dtype == RMSNORM_BF16 ? launch_rope_vec_bf16
+                                             : launch_rope_vec_f16;
+    bool taken = false;
+    const cudaError_t err = vec(a, &taken);
+    if (taken)
+        return err;
     return dtype == RMSNORM_F32    ? launch_scalar<RMSNORM_F32>(a)
            : dtype == RMSNORM_BF16 ? launch_scalar<RMSNORM_BF16>(a)
                                    : launch_scalar<RMSNORM_F16>(a);

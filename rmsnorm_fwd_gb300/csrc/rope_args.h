@@ -50,6 +50,10 @@ struct RopeArgs {
     int sm_count;
 };
 cudaError_t launch_rope(const RopeArgs &a, int dtype);
+// The vector bodies; *taken is false when none takes the call.
+cudaError_t launch_rope_vec_f32(const RopeArgs &a, bool *taken);
+cudaError_t launch_rope_vec_bf16(const RopeArgs &a, bool *taken);
+cudaError_t launch_rope_vec_f16(const RopeArgs &a, bool *taken);
 
 struct RopeBwdArgs {
     LaunchArgs base;
