@@ -47,6 +47,34 @@ __device__ inline RowScale row_scale(float S, float n, float eps, Resum resum)
     return f;
 }
 
+// The gradient bodies that keep x in registers form sum(du g x) before r is
+// known, so they trust the plain sum S in a narrower range: S <= 2^80, and
+// S >= 2^-60 unless eps >= 2^-40 bounds r.  There no product of dy, g and x
+// leaves fp32's range for dy g within 2^+-60.  Otherwise x is replaced by k x
+// (k a power of two: exact but for elements below 2^-46 of the largest), eps
+// by eps k^2, and dx is multiplied by k at the end.  k keeps both the new sum
+// and eps k^2 finite: 2^-80 above; below, 2^100 where S < 2^-100 and
+// eps < 2^-120 (then S k^2 < 2^100, eps k^2 < 2^80, and the smallest element's
+// square is 2^-98), else 2^50 (S k^2 <= 2^40, eps k^2 < 2^60).
+template <int DT> __device__ inline bool bwd_rescales(float S, float eps)
+{
+    return kRangeGuard<DT> && !(S <= 0x1p80f && (S >= 0x1p-60f || eps >= 0x1p-40f));
+}
+__device__ inline float bwd_rescale_k(float S, float eps)
+{
+    return S > 0x1p80f ? 0x1p-80f : S < 0x1p-100f && eps < 0x1p-120f ? 0x1p100f : 0x1p50f;
+}
+// x <- k x in the element type.
+template <int DT, int VB> __device__ inline void scale_by(Vec<VB> &v, float k)
+{
+#pragma unroll
+    for (int i = 0; i < Vec<VB>::kWords; ++i) {
+        float a, b = 0.f;
+        Elem<DT>::widen(v.w[i], a, b);
+        v.w[i] = Elem<DT>::narrow(a * k, b * k);
+    }
+}
+
 // ---- heads in vectors
 //
 // A head is cut into slots of two VB-byte vectors, so that a slot holds whole
@@ -150,6 +178,165 @@ __device__ inline void slot_vectors(int p, int slots, int half_v, bool interleav
         va = turned ? p : p + half_v;
         vb = va + (turned ? half_v : slots - half_v);
     }
+}
+
+// The pairing of the rotated elements, compiled apart: halves over the whole
+// head, halves over a part of it, neighbours (over any part).
+enum { kHalvesFull = 0, kHalves = 1, kInterleaved = 2 };
+
+// ---- couples
+
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ inline uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
+// Loads at their place (volatile: they are not moved up into registers that
+// wait): C = 2 or 4 floats, C elements of a weight widened.
+template <int C> __device__ inline void ld_floats(float (&f)[C], const float *p)
+{
+    if constexpr (C == 4)
+        asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                     : "l"(p));
+    else if constexpr (C == 2)
+        asm volatile("ld.global.nc.v2.f32 {%0,%1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "l"(p));
+    else
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f[0]) : "l"(p));
+}
+template <int DT, int C> __device__ inline void ld_weights(float (&f)[C], const char *w)
+{
+    if constexpr (Elem<DT>::kPerWord == 1) {
+        ld_floats(f, reinterpret_cast<const float *>(w));
+    } else {
+        Vec<2 * C> v;
+        if constexpr (C == 4)
+            asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(v.w[0]), "=r"(v.w[1])
+                         : "l"(w));
+        else
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.w[0]) : "l"(w));
+        widen_vec<DT, 2 * C>(f, v);
+    }
+}
+
+// Elements e .. e + C of a slot's two vectors (C = 2 or 4), or of their
+// weights, as packed couples (A_i, B_i) of which A_i is to be rotated with B_i:
+// halves: A from the first vector and B from the second; neighbours: A the
+// even elements and B the odd ones.
+template <int C, bool INTER>
+__device__ inline void couple(uint64_t (&A)[C / 2], uint64_t (&B)[C / 2], const float (&a)[C],
+                              const float (&b)[C])
+{
+    if constexpr (!INTER) {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            A[i] = f2(a[2 * i], a[2 * i + 1]);
+            B[i] = f2(b[2 * i], b[2 * i + 1]);
+        }
+    } else if constexpr (C == 4) {
+        A[0] = f2(a[0], a[2]), B[0] = f2(a[1], a[3]);
+        A[1] = f2(b[0], b[2]), B[1] = f2(b[1], b[3]);
+    } else {
+        A[0] = f2(a[0], b[0]), B[0] = f2(a[1], b[1]);
+    }
+}
+template <int C, bool INTER>
+__device__ inline void uncouple(float (&a)[C], float (&b)[C], const uint64_t (&A)[C / 2],
+                                const uint64_t (&B)[C / 2])
+{
+    if constexpr (!INTER) {
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            f2split(A[i], a[2 * i], a[2 * i + 1]);
+            f2split(B[i], b[2 * i], b[2 * i + 1]);
+        }
+    } else if constexpr (C == 4) {
+        f2split(A[0], a[0], a[2]), f2split(B[0], a[1], a[3]);
+        f2split(A[1], b[0], b[2]), f2split(B[1], b[1], b[3]);
+    } else {
+        f2split(A[0], a[0], b[0]), f2split(B[0], a[1], b[1]);
+    }
+}
+// The cosines (or sines) of the couples: halves from pa + e, neighbours from
+// pa + e / 2 for the first vector and pb + e / 2 for the second.
+template <int C, bool INTER>
+__device__ inline void ld_couples(uint64_t (&c)[C / 2], const float *pa, const float *pb, int e,
+                                  bool on_a, bool on_b)
+{
+    if constexpr (!INTER) {
+        float f[C] = {};
+        if (on_a)
+            ld_floats(f, pa + e);
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i)
+            c[i] = f2(f[2 * i], f[2 * i + 1]);
+    } else {
+        float f0[C / 2] = {}, f1[C / 2] = {};
+        if (on_a)
+            ld_floats(f0, pa + e / 2);
+        if (on_b)
+            ld_floats(f1, pb + e / 2);
+        if constexpr (C == 4)
+            c[0] = f2(f0[0], f0[1]), c[1] = f2(f1[0], f1[1]);
+        else
+            c[0] = f2(f0[0], f1[0]);
+    }
+}
+// all-ones where a couple is rotated, of the two elements it holds
+template <int C, bool INTER>
+__device__ inline uint64_t couple_mask(int i, bool on_a, bool on_b)
+{
+    if constexpr (!INTER)
+        return on_a ? ~0ull : 0ull;
+    else if constexpr (C == 4)
+        return (i == 0 ? on_a : on_b) ? ~0ull : 0ull;
+    else
+        return (on_a ? 0xFFFFFFFFull : 0ull) | (on_b ? 0xFFFFFFFFull << 32 : 0ull);
+}
+
+// Elements e .. e + C of a vector.
+template <int DT, int VB, int C>
+__device__ inline void get(float (&f)[C], const Vec<VB> &v, int e)
+{
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+        if constexpr (Elem<DT>::kPerWord == 2) {
+            Elem<DT>::widen(v.w[e / 2 + i], f[2 * i], f[2 * i + 1]);
+        } else {
+            f[2 * i] = __uint_as_float(v.w[e + 2 * i]);
+            f[2 * i + 1] = __uint_as_float(v.w[e + 2 * i + 1]);
+        }
+    }
+}
+// Elements e .. e + C back in the element type.
+template <int DT, int VB, int C>
+__device__ inline void put(Vec<VB> &v, int e, const float (&f)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+        if constexpr (Elem<DT>::kPerWord == 2) {
+            v.w[e / 2 + i] = Elem<DT>::narrow(f[2 * i], f[2 * i + 1]);
+        } else {
+            v.w[e + 2 * i] = __float_as_uint(f[2 * i]);
+            v.w[e + 2 * i + 1] = __float_as_uint(f[2 * i + 1]);
+        }
+    }
+}
+
+// ---- host: alignment of a call's tensors
+
+inline bool multiple(int64_t v, int64_t of) { return v % of == 0; }
+inline bool aligned(const void *p, int64_t to)
+{
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(to) == 0;
+}
+inline bool view_aligned(const HeadsView &v, int64_t es, int64_t to)
+{
+    return aligned(v.p, to) && multiple(v.ts * es, to) && multiple(v.hs * es, to);
 }
 
 } // namespace rmsnorm

@@ -9,10 +9,6 @@
 namespace rmsnorm {
 namespace {
 
-// The pairing of the rotated elements, compiled apart: halves over the whole
-// head, halves over a part of it, neighbours (over any part).
-enum { kHalvesFull = 0, kHalves = 1, kInterleaved = 2 };
-
 // N codes from a vector's first words, in one store.
 template <int N, int VB> __device__ inline void st_e4m3(char *dst, const Vec<VB> &v)
 {
@@ -23,150 +19,16 @@ template <int N, int VB> __device__ inline void st_e4m3(char *dst, const Vec<VB>
     st_codes<N>(dst, w);
 }
 
-__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ inline uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
-
-// Loads at their place (volatile: they are not moved up into registers that
-// wait): C = 2 or 4 floats, C elements of a weight widened.
-template <int C> __device__ inline void ld_floats(float (&f)[C], const float *p)
-{
-    if constexpr (C == 4)
-        asm volatile("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                     : "l"(p));
-    else if constexpr (C == 2)
-        asm volatile("ld.global.nc.v2.f32 {%0,%1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "l"(p));
-    else
-        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f[0]) : "l"(p));
-}
-template <int DT, int C> __device__ inline void ld_weights(float (&f)[C], const char *w)
-{
-    if constexpr (Elem<DT>::kPerWord == 1) {
-        ld_floats(f, reinterpret_cast<const float *>(w));
-    } else {
-        Vec<2 * C> v;
-        if constexpr (C == 4)
-            asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];"
-                         : "=r"(v.w[0]), "=r"(v.w[1])
-                         : "l"(w));
-        else
-            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v.w[0]) : "l"(w));
-        widen_vec<DT, 2 * C>(f, v);
-    }
-}
-
-// Elements e .. e + C of a slot's two vectors (C = 2 or 4), or of their
-// weights, as packed couples (A_i, B_i) of which A_i is to be rotated with B_i:
-// halves: A from the first vector and B from the second; neighbours: A the
-// even elements and B the odd ones.
-template <int C, bool INTER>
-__device__ inline void couple(uint64_t (&A)[C / 2], uint64_t (&B)[C / 2], const float (&a)[C],
-                              const float (&b)[C])
-{
-    if constexpr (!INTER) {
-#pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-            A[i] = f2(a[2 * i], a[2 * i + 1]);
-            B[i] = f2(b[2 * i], b[2 * i + 1]);
-        }
-    } else if constexpr (C == 4) {
-        A[0] = f2(a[0], a[2]), B[0] = f2(a[1], a[3]);
-        A[1] = f2(b[0], b[2]), B[1] = f2(b[1], b[3]);
-    } else {
-        A[0] = f2(a[0], b[0]), B[0] = f2(a[1], b[1]);
-    }
-}
-template <int C, bool INTER>
-__device__ inline void uncouple(float (&a)[C], float (&b)[C], const uint64_t (&A)[C / 2],
-                                const uint64_t (&B)[C / 2])
-{
-    if constexpr (!INTER) {
-#pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-            f2split(A[i], a[2 * i], a[2 * i + 1]);
-            f2split(B[i], b[2 * i], b[2 * i + 1]);
-        }
-    } else if constexpr (C == 4) {
-        f2split(A[0], a[0], a[2]), f2split(B[0], a[1], a[3]);
-        f2split(A[1], b[0], b[2]), f2split(B[1], b[1], b[3]);
-    } else {
-        f2split(A[0], a[0], b[0]), f2split(B[0], a[1], b[1]);
-    }
-}
-// The cosines (or sines) of the couples: halves from pa + e, neighbours from
-// pa + e / 2 for the first vector and pb + e / 2 for the second.
-template <int C, bool INTER>
-__device__ inline void ld_couples(uint64_t (&c)[C / 2], const float *pa, const float *pb, int e,
-                                  bool on_a, bool on_b)
-{
-    if constexpr (!INTER) {
-        float f[C] = {};
-        if (on_a)
-            ld_floats(f, pa + e);
-#pragma unroll
-        for (int i = 0; i < C / 2; ++i)
-            c[i] = f2(f[2 * i], f[2 * i + 1]);
-    } else {
-        float f0[C / 2] = {}, f1[C / 2] = {};
-        if (on_a)
-            ld_floats(f0, pa + e / 2);
-        if (on_b)
-            ld_floats(f1, pb + e / 2);
-        if constexpr (C == 4)
-            c[0] = f2(f0[0], f0[1]), c[1] = f2(f1[0], f1[1]);
-        else
-            c[0] = f2(f0[0], f1[0]);
-    }
-}
-// all-ones where a couple is rotated, of the two elements it holds
-template <int C, bool INTER>
-__device__ inline uint64_t couple_mask(int i, bool on_a, bool on_b)
-{
-    if constexpr (!INTER)
-        return on_a ? ~0ull : 0ull;
-    else if constexpr (C == 4)
-        return (i == 0 ? on_a : on_b) ? ~0ull : 0ull;
-    else
-        return (on_a ? 0xFFFFFFFFull : 0ull) | (on_b ? 0xFFFFFFFFull << 32 : 0ull);
-}
-
-// Elements e .. e + C of a vector, and back in the element type or as E4M3
-// codes of value * inv (in word e / 4).
-template <int DT, int VB, int C>
-__device__ inline void get(float (&f)[C], const Vec<VB> &v, int e)
-{
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i) {
-        if constexpr (Elem<DT>::kPerWord == 2) {
-            Elem<DT>::widen(v.w[e / 2 + i], f[2 * i], f[2 * i + 1]);
-        } else {
-            f[2 * i] = __uint_as_float(v.w[e + 2 * i]);
-            f[2 * i + 1] = __uint_as_float(v.w[e + 2 * i + 1]);
-        }
-    }
-}
+// Elements e .. e + C back in the element type or as E4M3 codes of value * inv
+// (in word e / 4).
 template <int DT, int VB, int C>
 __device__ inline void put(Vec<VB> &v, int e, const float (&f)[C], bool code, float inv)
 {
-    if (code) {
+    if (code)
         v.w[e / 4] = e4m3x4(f[0] * inv, f[1] * inv, C == 4 ? f[C - 2] * inv : 0.f,
                             C == 4 ? f[C - 1] * inv : 0.f);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i) {
-        if constexpr (Elem<DT>::kPerWord == 2) {
-            v.w[e / 2 + i] = Elem<DT>::narrow(f[2 * i], f[2 * i + 1]);
-        } else {
-            v.w[e + 2 * i] = __float_as_uint(f[2 * i]);
-            v.w[e + 2 * i + 1] = __float_as_uint(f[2 * i + 1]);
-        }
-    }
+    else
+        put<DT, VB, C>(v, e, f);
 }
 
 // How a call's heads are cut into warps: parts of per heads each, q's, then
@@ -412,16 +274,6 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     }
 }
 
-bool multiple(int64_t v, int64_t of) { return v % of == 0; }
-bool aligned(const void *p, int64_t to)
-{
-    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(to) == 0;
-}
-bool view_aligned(const HeadsView &v, int64_t es, int64_t to)
-{
-    return aligned(v.p, to) && multiple(v.ts * es, to) && multiple(v.hs * es, to);
-}
-
 constexpr int kMostSlots = 128; // 32 lanes with four slots each
 
 // Whether vectors of vb bytes can read and write every head of the call.
@@ -492,9 +344,10 @@ template <int DT, int VB, bool APPEND, int MODE> cudaError_t launch_lanes(const 
     }
     if (slots <= 32)
         return launch_vec<DT, VB, 32, 1, 1, APPEND, MODE>(a);
-    if (slots <= 64)
-        return launch_vec<DT, VB, 32, 2, 1, APPEND, MODE>(a);
-    return launch_vec<DT, VB, 32, 4, 1, APPEND, MODE>(a);
+    if constexpr (VB < 16 || Elem<DT>::kSize == 4)
+        if (slots > 64)
+            return launch_vec<DT, VB, 32, 4, 1, APPEND, MODE>(a);
+    return launch_vec<DT, VB, 32, 2, 1, APPEND, MODE>(a); // up to 64 (head_dim <= 1024)
 }
 
 template <int DT, int VB, bool APPEND> cudaError_t launch_mode(const RopeArgs &a)

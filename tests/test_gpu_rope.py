@@ -162,6 +162,20 @@ def test_extreme_heads(dtype, D, layout):
         R.assert_close(dkw, rk[2], rk[3], 129)
 
 
+def test_eps_zero_with_idle_lanes():
+    """Head counts that leave lanes of the last warp without a head, eps 0: no
+    zero of theirs is divided by the square root of zero."""
+    for hq, hk, D in ((3, 1, 128), (5, 2, 64), (1, 1, 80), (3, 1, 72)):
+        c, g = make("bf16", 9, hq, hk, D, D, "plain", 8)
+        dy_q, dy_k = R.rand(g, (9, hq, D), torch.bfloat16), R.rand(g, (9, hk, D), torch.bfloat16)
+        got = rn.qk_norm_rope_backward(dy_q, dy_k, c["q"], c["k"], c["qw"], c["kw"], c["cs"],
+                                       c["pos"], 0.0)
+        for i, (dy, x, w) in enumerate(((dy_q, c["q"], c["qw"]), (dy_k, c["k"], c["kw"]))):
+            ref = R.heads_bwd(dy, x, w, 0.0, 0.0, c["rows"], False)
+            R.assert_close(got[i], ref[0], ref[1], K_DX)
+            R.assert_close(got[2 + i], ref[2], ref[3], 129)
+
+
 # ------------------------------------------------------------------ positions outside the table
 
 def test_positions_outside_the_table():
