@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const ColSum a, const ColS
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     float s = 0.f;
     if (col0 + tx < c.cols)
+#pragma unroll 8
         for (int64_t r = ty; r < c.rows; r += 32)
             s += c.part[r * c.ld + col0 + tx];
     sums[ty][tx] = s;

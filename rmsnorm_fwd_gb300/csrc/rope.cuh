@@ -186,13 +186,32 @@ enum { kHalvesFull = 0, kHalves = 1, kInterleaved = 2 };
 
 // ---- couples
 
-__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+// Two fp32 values in one register pair, worked on by the packed instructions
+// (two IEEE operations each).
+struct Two {
+    uint64_t v;
+};
+__device__ inline Two two(float a, float b) { return {f2(a, b)}; }
+__device__ inline void untwo(Two p, float &a, float &b) { f2split(p.v, a, b); }
+__device__ inline Two operator*(Two p, Two q) { return {mul2(p.v, q.v)}; }
+__device__ inline Two operator*(Two p, float q) { return {mul2(p.v, f2(q, q))}; }
+__device__ inline Two operator+(Two p, Two q) { return {add2(p.v, q.v)}; }
+__device__ inline Two operator+(Two p, float q) { return {add2(p.v, f2(q, q))}; }
+__device__ inline Two operator-(Two p) { return {p.v ^ 0x8000000080000000ull}; }
+__device__ inline Two fma2(Two p, Two q, Two c)
 {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(p.v), "l"(q.v), "l"(c.v));
     return r;
 }
-__device__ inline uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
+__device__ inline Two fma2(Two p, float q, Two c) { return fma2(p, two(q, q), c); }
+// Which of the two are rotated: the others are 0 (pick), or 1 in place of 0
+// (or_one).
+struct Which {
+    uint64_t mask;
+};
+__device__ inline Two pick(Two p, Which w) { return {p.v & w.mask}; }
+__device__ inline Two or_one(Two p, Which w) { return {p.v | (~w.mask & f2(1.f, 1.f))}; }
 
 // Loads at their place (volatile: they are not moved up into registers that
 // wait): C = 2 or 4 floats, C elements of a weight widened.
@@ -224,47 +243,47 @@ template <int DT, int C> __device__ inline void ld_weights(float (&f)[C], const 
 }
 
 // Elements e .. e + C of a slot's two vectors (C = 2 or 4), or of their
-// weights, as packed couples (A_i, B_i) of which A_i is to be rotated with B_i:
+// weights, as couples (A_i, B_i) of which A_i is to be rotated with B_i:
 // halves: A from the first vector and B from the second; neighbours: A the
 // even elements and B the odd ones.
 template <int C, bool INTER>
-__device__ inline void couple(uint64_t (&A)[C / 2], uint64_t (&B)[C / 2], const float (&a)[C],
+__device__ inline void couple(Two (&A)[C / 2], Two (&B)[C / 2], const float (&a)[C],
                               const float (&b)[C])
 {
     if constexpr (!INTER) {
 #pragma unroll
         for (int i = 0; i < C / 2; ++i) {
-            A[i] = f2(a[2 * i], a[2 * i + 1]);
-            B[i] = f2(b[2 * i], b[2 * i + 1]);
+            A[i] = two(a[2 * i], a[2 * i + 1]);
+            B[i] = two(b[2 * i], b[2 * i + 1]);
         }
     } else if constexpr (C == 4) {
-        A[0] = f2(a[0], a[2]), B[0] = f2(a[1], a[3]);
-        A[1] = f2(b[0], b[2]), B[1] = f2(b[1], b[3]);
+        A[0] = two(a[0], a[2]), B[0] = two(a[1], a[3]);
+        A[1] = two(b[0], b[2]), B[1] = two(b[1], b[3]);
     } else {
-        A[0] = f2(a[0], b[0]), B[0] = f2(a[1], b[1]);
+        A[0] = two(a[0], b[0]), B[0] = two(a[1], b[1]);
     }
 }
 template <int C, bool INTER>
-__device__ inline void uncouple(float (&a)[C], float (&b)[C], const uint64_t (&A)[C / 2],
-                                const uint64_t (&B)[C / 2])
+__device__ inline void uncouple(float (&a)[C], float (&b)[C], const Two (&A)[C / 2],
+                                const Two (&B)[C / 2])
 {
     if constexpr (!INTER) {
 #pragma unroll
         for (int i = 0; i < C / 2; ++i) {
-            f2split(A[i], a[2 * i], a[2 * i + 1]);
-            f2split(B[i], b[2 * i], b[2 * i + 1]);
+            untwo(A[i], a[2 * i], a[2 * i + 1]);
+            untwo(B[i], b[2 * i], b[2 * i + 1]);
         }
     } else if constexpr (C == 4) {
-        f2split(A[0], a[0], a[2]), f2split(B[0], a[1], a[3]);
-        f2split(A[1], b[0], b[2]), f2split(B[1], b[1], b[3]);
+        untwo(A[0], a[0], a[2]), untwo(B[0], a[1], a[3]);
+        untwo(A[1], b[0], b[2]), untwo(B[1], b[1], b[3]);
     } else {
-        f2split(A[0], a[0], b[0]), f2split(B[0], a[1], b[1]);
+        untwo(A[0], a[0], b[0]), untwo(B[0], a[1], b[1]);
     }
 }
 // The cosines (or sines) of the couples: halves from pa + e, neighbours from
 // pa + e / 2 for the first vector and pb + e / 2 for the second.
 template <int C, bool INTER>
-__device__ inline void ld_couples(uint64_t (&c)[C / 2], const float *pa, const float *pb, int e,
+__device__ inline void ld_couples(Two (&c)[C / 2], const float *pa, const float *pb, int e,
                                   bool on_a, bool on_b)
 {
     if constexpr (!INTER) {
@@ -273,7 +292,7 @@ __device__ inline void ld_couples(uint64_t (&c)[C / 2], const float *pa, const f
             ld_floats(f, pa + e);
 #pragma unroll
         for (int i = 0; i < C / 2; ++i)
-            c[i] = f2(f[2 * i], f[2 * i + 1]);
+            c[i] = two(f[2 * i], f[2 * i + 1]);
     } else {
         float f0[C / 2] = {}, f1[C / 2] = {};
         if (on_a)
@@ -281,21 +300,21 @@ __device__ inline void ld_couples(uint64_t (&c)[C / 2], const float *pa, const f
         if (on_b)
             ld_floats(f1, pb + e / 2);
         if constexpr (C == 4)
-            c[0] = f2(f0[0], f0[1]), c[1] = f2(f1[0], f1[1]);
+            c[0] = two(f0[0], f0[1]), c[1] = two(f1[0], f1[1]);
         else
-            c[0] = f2(f0[0], f1[0]);
+            c[0] = two(f0[0], f1[0]);
     }
 }
-// all-ones where a couple is rotated, of the two elements it holds
+// Which of couple i's elements are rotated.
 template <int C, bool INTER>
-__device__ inline uint64_t couple_mask(int i, bool on_a, bool on_b)
+__device__ inline Which rotated(int i, bool on_a, bool on_b)
 {
     if constexpr (!INTER)
-        return on_a ? ~0ull : 0ull;
+        return {on_a ? ~0ull : 0ull};
     else if constexpr (C == 4)
-        return (i == 0 ? on_a : on_b) ? ~0ull : 0ull;
+        return {(i == 0 ? on_a : on_b) ? ~0ull : 0ull};
     else
-        return (on_a ? 0xFFFFFFFFull : 0ull) | (on_b ? 0xFFFFFFFFull << 32 : 0ull);
+        return {(on_a ? 0xFFFFFFFFull : 0ull) | (on_b ? 0xFFFFFFFFull << 32 : 0ull)};
 }
 
 // Elements e .. e + C of a vector.

@@ -13,21 +13,11 @@
 
 namespace rmsnorm {
 
-#ifndef MINB
-#define MINB 4
-#endif
-#ifndef STAGES
-#define STAGES 3
-#endif
-#ifndef ITERS
-#define ITERS 4
-#endif
-#ifndef ITEMS
-#define ITEMS 8
-#endif
-// A workspace row per block: MINB blocks on every SM, and one more for each
-// tensor's rounding.
-int rope_bwd_max_blocks(int sm_count) { return MINB * sm_count + 2; }
+constexpr int kBwdBlocksPerSm = 4; // of 128 threads with up to 128 registers
+
+// A workspace row per block: all SMs' blocks, and one more for each tensor's
+// rounding.
+int rope_bwd_max_blocks(int sm_count) { return kBwdBlocksPerSm * sm_count + 2; }
 
 namespace {
 
@@ -143,11 +133,22 @@ __global__ void __launch_bounds__(256) rope_bwd_scalar_kernel(const RopeBwdArgs 
 
 // ---- heads in vectors (rope.cuh)
 //
-// Each lane copies its own vectors of x and dy ahead into a ring in shared
-// memory (cp.async; no lane reads another's, so only its own copies are
-// waited for), which keeps the bytes on the way out of the registers that
-// dw's sums, the angles and the weights take.  A warp keeps to one tensor and
-// goes through chunks of a token's heads, 32 / TPR at a time.
+// A warp keeps to one tensor and goes through a run of consecutive steps, 32 /
+// TPR heads of a token each.  Every lane copies its own vectors of x and dy
+// ahead into a ring in shared memory (cp.async; no lane reads another's, so
+// only its own copies are waited for): the bytes on the way take no registers,
+// which dw's sums, the angles and g fill.  The angles are loaded once a token.
+//
+// What bounds it: instructions first (the same time without its loads or
+// stores), memory close behind.  Measured with launch_colsum (16384 tokens of
+// 32 + 8 bf16 heads of 128, 505 MB, floor 75.7 us at the copy bandwidth): scalar
+// body 521 us, this one 86.8 us (5.83 TB/s, 87 %).  On the way: warps that take
+// short chunks of many tokens in turn 96.8 us (61 M warp instructions for 49 M: a
+// division and the angles every chunk); two passes over x and dy in registers,
+// 24 warps an SM and no ring, 114 us (67 M: widening and angles twice), the same
+// without the packed instructions 122 us (81 M).  128 registers and 16 warps an SM
+// (96 and 20: 114 us, spills); 3 stages (4: 92.9 us: the larger ring leaves L1 no
+// room for the angles).
 
 template <int VB> __device__ inline void cp_async(uint32_t dst, const void *src)
 {
@@ -173,38 +174,15 @@ template <int VB> __device__ inline void ld_ring(Vec<VB> &v, uint32_t p)
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.w[0]) : "r"(p) : "memory");
 }
 
-// How tokens' heads are cut: chunks of a token's heads, iters steps of
-// 32 / TPR heads each.
-struct Chunks {
-    uint32_t per_token, iters;
-};
-
-// A warp's place in its chunks.
-struct Cursor {
-    uint32_t item, tok, step, end; // step .. end: steps of the token in this chunk
-    __device__ inline void start(uint32_t i, const Chunks &c, uint32_t steps)
-    {
-        item = i;
-        tok = i / c.per_token;
-        step = (i - tok * c.per_token) * c.iters;
-        end = min(step + c.iters, steps);
-    }
-    __device__ inline void next(uint32_t stride, const Chunks &c, uint32_t steps)
-    {
-        if (++step == end)
-            start(item + stride, c, steps);
-    }
-};
-
 template <int DT, int VB, int TPR, int NP, int MODE>
-__global__ void __launch_bounds__(kBwdThreads, NP == 1 ? MINB : 1)
-rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks qc, Chunks kc)
+__global__ void __launch_bounds__(kBwdThreads, NP == 1 ? kBwdBlocksPerSm : 1)
+rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
 {
     using E = Elem<DT>;
     constexpr int N = kVpe<DT, VB>;
     constexpr int G = 32 / TPR;
     constexpr int C = N < 4 ? N : 4;
-    constexpr int S = NP == 1 ? STAGES : NP == 2 ? 2 : 1; // ring stages
+    constexpr int S = NP == 1 ? 3 : NP == 2 ? 2 : 1; // ring stages
     constexpr int kAhead = S > 1 ? S - 1 : 1;        // steps asked for ahead
     constexpr int kStage = NP * 4 * 32 * VB;         // bytes of a warp's stage
     constexpr int kWarps = kBwdThreads / 32;
@@ -214,70 +192,95 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = lane % TPR, g = lane / TPR;
     const bool isq = static_cast<int>(blockIdx.x) < split.q;
-    const Chunks ch = isq ? qc : kc;
     const int heads = isq ? a.q_heads : a.k_heads;
-    const uint32_t steps = (heads + G - 1) / G;
-    const uint32_t items = static_cast<uint32_t>(a.tokens) * ch.per_token;
-    const uint32_t block = isq ? blockIdx.x : blockIdx.x - split.q;
-    const uint32_t stride = (isq ? split.q : split.k) * kWarps;
+    const uint32_t steps = (heads + G - 1) / G; // of a token
     const int slots = a.head_dim / (2 * N), half_v = a.rope.rd / (2 * N);
     const char *xb = isq ? a.q.p : a.k.p, *yb = isq ? a.qdy.p : a.kdy.p;
     char *ob = isq ? a.dq.p : a.dk.p;
-    const int64_t xts = isq ? a.q.ts : a.k.ts, xhs = isq ? a.q.hs : a.k.hs;
-    const int64_t yts = isq ? a.qdy.ts : a.kdy.ts, yhs = isq ? a.qdy.hs : a.kdy.hs;
-    const int64_t ots = isq ? a.dq.ts : a.dk.ts, ohs = isq ? a.dq.hs : a.dk.hs;
-    const RowCount n = row_count(a.head_dim);
+    const int64_t xts = (isq ? a.q.ts : a.k.ts) * E::kSize, xhs = (isq ? a.q.hs : a.k.hs) * E::kSize;
+    const int64_t yts = (isq ? a.qdy.ts : a.kdy.ts) * E::kSize,
+                  yhs = (isq ? a.qdy.hs : a.kdy.hs) * E::kSize;
+    const int64_t ots = (isq ? a.dq.ts : a.dk.ts) * E::kSize,
+                  ohs = (isq ? a.dq.hs : a.dk.hs) * E::kSize;
+    const float inv_n = 1.f / static_cast<float>(a.head_dim);
     int va[NP], vb[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j)
         slot_vectors(t + j * TPR, slots, half_v, inter, va[j], vb[j]);
 
-    // This lane's weights, and its sums of dw as couples.
-    Vec<VB> w[NP][2];
-    uint64_t accA[NP][N / 2], accB[NP][N / 2];
+    // This warp's steps: an even share of the tensor's, in order.
+    uint32_t left, first;
+    {
+        const uint64_t all = static_cast<uint64_t>(a.tokens) * steps;
+        const uint64_t block = isq ? blockIdx.x : blockIdx.x - split.q;
+        const uint64_t warps = static_cast<uint64_t>(isq ? split.q : split.k) * kWarps;
+        const uint64_t i = block * kWarps + __shfl_sync(0xFFFFFFFFu, warp, 0);
+        first = static_cast<uint32_t>(all * i / warps);
+        left = static_cast<uint32_t>(all * (i + 1) / warps) - first;
+    }
+
+    // This lane's g = w + bias, and its sums of dw, as couples.
+    Two gA[NP][N / 2], gB[NP][N / 2], accA[NP][N / 2], accB[NP][N / 2];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-        vzero(w[j][0]);
-        vzero(w[j][1]);
+        Vec<VB> w[2];
+        vzero(w[0]);
+        vzero(w[1]);
         if (t + j * TPR < slots) {
             const char *ws = static_cast<const char *>(isq ? a.qw : a.kw);
-            ld_const(w[j][0], ws + va[j] * VB);
-            ld_const(w[j][1], ws + vb[j] * VB);
+            ld_const(w[0], ws + va[j] * VB);
+            ld_const(w[1], ws + vb[j] * VB);
         }
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-            accA[j][i] = accB[j][i] = 0;
+        for (int e = 0; e < N; e += C) {
+            float fa[C], fb[C];
+            Two A[C / 2], B[C / 2];
+            get<DT, VB, C>(fa, w[0], e);
+            get<DT, VB, C>(fb, w[1], e);
+            couple<C, inter>(A, B, fa, fb);
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+                gA[j][e / 2 + i] = A[i] + a.bias;
+                gB[j][e / 2 + i] = B[i] + a.bias;
+                accA[j][e / 2 + i] = accB[j][e / 2 + i] = two(0.f, 0.f);
+            }
+        }
     }
 
     const uint32_t my = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
                         warp * (S * kStage) + lane * VB;
+    // The step asked for next, and the step worked on.
+    uint32_t tok_in = first / steps, in = first - tok_in * steps, left_in = left;
+    uint32_t tok = tok_in, step = in;
+    const char *px = xb + tok_in * xts + (int64_t(in) * G + g) * xhs;
+    const char *py = yb + tok_in * yts + (int64_t(in) * G + g) * yhs;
+    char *po = ob + tok * ots + (int64_t(step) * G + g) * ohs;
     // Asks a step's vectors into a stage (its two vectors of x, then of dy).
-    auto ask = [&](const Cursor &c, uint32_t stage) {
-        const int h = static_cast<int>(c.step) * G + g;
-        if (c.item < items && h < heads) {
-            const char *x = xb + (c.tok * xts + h * xhs) * E::kSize;
-            const char *y = yb + (c.tok * yts + h * yhs) * E::kSize;
+    auto ask_next = [&](uint32_t stage) {
+        if (left_in) {
+            if (static_cast<int>(in) * G + g < heads) {
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                if (t + j * TPR >= slots)
-                    continue;
-                const uint32_t p = my + stage * kStage + j * (4 * 32 * VB);
-                cp_async<VB>(p, x + va[j] * VB);
-                cp_async<VB>(p + 32 * VB, x + vb[j] * VB);
-                cp_async<VB>(p + 64 * VB, y + va[j] * VB);
-                cp_async<VB>(p + 96 * VB, y + vb[j] * VB);
+                for (int j = 0; j < NP; ++j) {
+                    if (t + j * TPR >= slots)
+                        continue;
+                    const uint32_t p = my + stage * kStage + j * (4 * 32 * VB);
+                    cp_async<VB>(p, px + va[j] * VB);
+                    cp_async<VB>(p + 32 * VB, px + vb[j] * VB);
+                    cp_async<VB>(p + 64 * VB, py + va[j] * VB);
+                    cp_async<VB>(p + 96 * VB, py + vb[j] * VB);
+                }
+            }
+            --left_in;
+            px += G * xhs;
+            py += G * yhs;
+            if (++in == steps) {
+                in = 0;
+                ++tok_in;
+                px = xb + tok_in * xts + g * xhs;
+                py = yb + tok_in * yts + g * yhs;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-
-    Cursor at, ahead;
-    at.start(block * kWarps + warp, ch, steps);
-    ahead = at;
-    auto ask_next = [&](uint32_t stage) {
-        ask(ahead, stage);
-        if (ahead.item < items)
-            ahead.next(stride, ch, steps);
     };
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
@@ -285,17 +288,16 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
     uint32_t stage = 0;
     bool fresh = true, bad = false;
     // The token's angles as the couples take them.
-    uint64_t cc[NP][N / 2], ss[NP][N / 2];
-    int64_t next_pos = a.rope.rd && at.item < items ? a.rope.pos[at.tok] : 0;
-    while (at.item < items) {
+    Two cc[NP][N / 2], ss[NP][N / 2];
+    int64_t next_pos = a.rope.rd && left ? a.rope.pos[tok] : 0;
+    for (; left; --left) {
         if (fresh) {
             const int64_t pos = next_pos;
             bad = a.rope.rd && (pos < 0 || pos >= a.rope.max_pos);
-            if (bad && lane == 0 && at.step == 0)
+            if (bad && lane == 0)
                 record_bad_index(a.base.status);
-            const uint32_t after = at.item + stride;
-            if (a.rope.rd && after < items)
-                next_pos = a.rope.pos[after / ch.per_token];
+            if (a.rope.rd && tok + 1 < a.tokens)
+                next_pos = a.rope.pos[tok + 1];
             const float *cs = a.rope.cs + (bad ? 0 : pos) * a.rope.rd;
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -307,13 +309,12 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
                 const float *cb = cs + vb[j] * (N / 2);
 #pragma unroll
                 for (int e = 0; e < N; e += C) {
-                    uint64_t c[C / 2], s[C / 2];
+                    Two c[C / 2], s[C / 2];
                     ld_couples<C, inter>(c, ca, cb, e, on_a, on_b);
                     ld_couples<C, inter>(s, ca + a.rope.rd / 2, cb + a.rope.rd / 2, e, on_a, on_b);
 #pragma unroll
                     for (int i = 0; i < C / 2; ++i) {
-                        const uint64_t on = couple_mask<C, inter>(i, on_a, on_b);
-                        cc[j][e / 2 + i] = c[i] | (~on & f2(1.f, 1.f));
+                        cc[j][e / 2 + i] = or_one(c[i], rotated<C, inter>(i, on_a, on_b));
                         ss[j][e / 2 + i] = s[i];
                     }
                 }
@@ -321,8 +322,7 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
         }
         // All but the newest kAhead - 1 of this lane's groups have arrived.
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        const int h = static_cast<int>(at.step) * G + g;
-        const bool live = h < heads;
+        const bool live = static_cast<int>(step) * G + g < heads;
         Vec<VB> x[NP][2], y[NP][2];
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
@@ -343,89 +343,94 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
             ask_next(stage == 0 ? S - 1 : stage - 1);
         stage = stage + 1 == S ? 0 : stage + 1;
         if (!bad) {
-            float sum = 0.f;
+            // du, and the two sums of a head: x^2 and du g x.
+            Two dA[NP][N / 2], dB[NP][N / 2], xA[NP][N / 2], xB[NP][N / 2];
+            Two dotA = two(0.f, 0.f), dotB = dotA;
+            float sq[2] = {};
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
-                sum = sumsq_mixed<DT, VB>(x[j][1], sumsq_mixed<DT, VB>(x[j][0], sum));
-            // A group without a head keeps finite numbers: its zeros are summed.
-            sum = group_allreduce<TPR>(sum);
-            if (!live)
-                sum = 1.f;
-            float r = row_factor(sum, n, a.eps), k = 1.f;
-            const bool redo = bwd_rescales<DT>(sum, a.eps);
-            const bool rare = kRangeGuard<DT> && __any_sync(0xFFFFFFFFu, redo);
-            if (rare) {
-                const float kk = redo ? bwd_rescale_k(sum, a.eps) : 1.f;
-                float sk = 0.f;
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    scale_by<DT, VB>(x[j][0], kk);
-                    scale_by<DT, VB>(x[j][1], kk);
-                    sk = sumsq<DT, VB>(x[j][1], sumsq<DT, VB>(x[j][0], sk));
-                }
-                k = kk;
-                r = row_factor(group_allreduce<TPR>(sk), n, (a.eps * kk) * kk);
-            }
-            // du, and sum(du g x); dw's sums take du * (x r).
-            uint64_t eA[NP][N / 2], eB[NP][N / 2], dot = 0;
-            const uint64_t r2 = f2(r, r);
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
+            for (int j = 0; j < NP; ++j) {
+                const bool on_a = MODE == kHalvesFull ||
+                                  (inter ? va[j] * N < a.rope.rd : t + j * TPR < half_v);
+                const bool on_b = inter ? vb[j] * N < a.rope.rd : on_a;
+                sq[0] = sumsq_mixed<DT, VB>(x[j][0], sq[0]);
+                sq[1] = sumsq_mixed<DT, VB>(x[j][1], sq[1]);
 #pragma unroll
                 for (int e = 0; e < N; e += C) {
                     float fa[C], fb[C];
-                    uint64_t gA[C / 2], gB[C / 2], xA[C / 2], xB[C / 2], yA[C / 2], yB[C / 2];
-                    get<DT, VB, C>(fa, w[j][0], e);
-                    get<DT, VB, C>(fb, w[j][1], e);
-                    couple<C, inter>(gA, gB, fa, fb);
+                    Two yA[C / 2], yB[C / 2], cA[C / 2], cB[C / 2];
                     get<DT, VB, C>(fa, x[j][0], e);
                     get<DT, VB, C>(fb, x[j][1], e);
-                    couple<C, inter>(xA, xB, fa, fb);
+                    couple<C, inter>(cA, cB, fa, fb);
                     get<DT, VB, C>(fa, y[j][0], e);
                     get<DT, VB, C>(fb, y[j][1], e);
                     couple<C, inter>(yA, yB, fa, fb);
-                    const bool on_a = MODE == kHalvesFull ||
-                                      (inter ? va[j] * N < a.rope.rd : t + j * TPR < half_v);
-                    const bool on_b = inter ? vb[j] * N < a.rope.rd : on_a;
 #pragma unroll
                     for (int i = 0; i < C / 2; ++i) {
-                        const uint64_t on = couple_mask<C, inter>(i, on_a, on_b);
-                        const uint64_t c = cc[j][e / 2 + i], s = ss[j][e / 2 + i];
-                        const uint64_t duA = fma2(yA[i], c, mul2(yB[i] & on, s));
-                        const uint64_t duB = fma2(yB[i], c, neg2(mul2(yA[i] & on, s)));
-                        const uint64_t b2 = f2(a.bias, a.bias);
-                        uint64_t &aA = accA[j][e / 2 + i], &aB = accB[j][e / 2 + i];
-                        aA = fma2(duA, mul2(xA[i], r2), aA);
-                        aB = fma2(duB, mul2(xB[i], r2), aB);
-                        eA[j][e / 2 + i] = mul2(duA, add2(gA[i], b2));
-                        eB[j][e / 2 + i] = mul2(duB, add2(gB[i], b2));
-                        dot = fma2(eA[j][e / 2 + i], xA[i], dot);
-                        dot = fma2(eB[j][e / 2 + i], xB[i], dot);
+                        const int m = e / 2 + i;
+                        const Which on = rotated<C, inter>(i, on_a, on_b);
+                        const Two c = cc[j][m], s = ss[j][m];
+                        xA[j][m] = cA[i];
+                        xB[j][m] = cB[i];
+                        dA[j][m] = fma2(yA[i], c, pick(yB[i], on) * s);
+                        dB[j][m] = fma2(yB[i], c, -(pick(yA[i], on) * s));
+                        dotA = fma2(dA[j][m] * gA[j][m], cA[i], dotA);
+                        dotB = fma2(dB[j][m] * gB[j][m], cB[i], dotB);
                     }
                 }
+            }
             float d0, d1;
-            f2split(dot, d0, d1);
-            const float total = group_allreduce<TPR>(d0 + d1);
-            // dx = r (e - x r m), m = r total / n
-            const float m = n.pow2 ? total * n.inv : total / n.n;
-            const float q = -(r * m) * r;
-            const uint64_t q2 = f2(q, q);
-            char *o = ob + (at.tok * ots + h * ohs) * E::kSize;
+            untwo(dotA + dotB, d0, d1);
+            float sum = sq[0] + sq[1], dot = d0 + d1;
+#pragma unroll
+            for (int off = TPR / 2; off > 0; off >>= 1) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+                dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
+            }
+            // A group without a head keeps finite numbers: its zeros are summed.
+            if (!live)
+                sum = 1.f;
+            float r = rsqrtf(fmaf(sum, inv_n, a.eps)), k = 1.f;
+            const bool redo = bwd_rescales<DT>(sum, a.eps);
+            const bool rare = kRangeGuard<DT> && __any_sync(0xFFFFFFFFu, redo);
+            if (rare) {
+                k = redo ? bwd_rescale_k(sum, a.eps) : 1.f;
+                Two s2 = two(0.f, 0.f), t2 = s2;
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int m = 0; m < N / 2; ++m) {
+                        xA[j][m] = xA[j][m] * k;
+                        xB[j][m] = xB[j][m] * k;
+                        s2 = fma2(xA[j][m], xA[j][m], fma2(xB[j][m], xB[j][m], s2));
+                        t2 = fma2(dA[j][m] * gA[j][m], xA[j][m], t2);
+                        t2 = fma2(dB[j][m] * gB[j][m], xB[j][m], t2);
+                    }
+                float s0, s1;
+                untwo(s2, s0, s1);
+                untwo(t2, d0, d1);
+                dot = group_allreduce<TPR>(d0 + d1);
+                s0 = group_allreduce<TPR>(s0 + s1);
+                r = rsqrtf(fmaf(live ? s0 : 1.f, inv_n, (a.eps * k) * k));
+            }
+            // xh = x r, dw += du xh, dx = r (du g - xh m), m = r sum(du g x) / n
+            const float m = r * (dot * inv_n);
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
+                Vec<VB> oa, ox;
 #pragma unroll
                 for (int e = 0; e < N; e += C) {
                     float fa[C], fb[C];
-                    uint64_t xA[C / 2], xB[C / 2];
-                    get<DT, VB, C>(fa, x[j][0], e);
-                    get<DT, VB, C>(fb, x[j][1], e);
-                    couple<C, inter>(xA, xB, fa, fb);
+                    Two A[C / 2], B[C / 2];
 #pragma unroll
                     for (int i = 0; i < C / 2; ++i) {
-                        xA[i] = mul2(fma2(xA[i], q2, eA[j][e / 2 + i]), r2);
-                        xB[i] = mul2(fma2(xB[i], q2, eB[j][e / 2 + i]), r2);
+                        const int v = e / 2 + i;
+                        const Two hA = xA[j][v] * r, hB = xB[j][v] * r;
+                        accA[j][v] = fma2(dA[j][v], hA, accA[j][v]);
+                        accB[j][v] = fma2(dB[j][v], hB, accB[j][v]);
+                        A[i] = fma2(hA, -m, dA[j][v] * gA[j][v]) * r;
+                        B[i] = fma2(hB, -m, dB[j][v] * gB[j][v]) * r;
                     }
-                    uncouple<C, inter>(fa, fb, xA, xB);
+                    uncouple<C, inter>(fa, fb, A, B);
                     if (rare) {
 #pragma unroll
                         for (int i = 0; i < C; ++i) {
@@ -433,20 +438,24 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
                             fb[i] *= k;
                         }
                     }
-                    put<DT, VB, C>(x[j][0], e, fa);
-                    put<DT, VB, C>(x[j][1], e, fb);
+                    put<DT, VB, C>(oa, e, fa);
+                    put<DT, VB, C>(ox, e, fb);
                 }
                 if (live && t + j * TPR < slots) {
-                    st_head(o + va[j] * VB, x[j][0]);
-                    st_head(o + vb[j] * VB, x[j][1]);
+                    st_head(po + va[j] * VB, oa);
+                    st_head(po + vb[j] * VB, ox);
                 }
             }
         }
         if constexpr (S == 1)
             ask_next(0);
-        const uint32_t item = at.item;
-        at.next(stride, ch, steps);
-        fresh = at.item != item;
+        po += G * ohs;
+        fresh = ++step == steps;
+        if (fresh) {
+            step = 0;
+            ++tok;
+            po = ob + tok * ots + g * ohs;
+        }
     }
     if (!a.part)
         return;
@@ -458,7 +467,7 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split, Chunks 
     for (int j = 0; j < NP; ++j)
 #pragma unroll
         for (int e = 0; e < N; e += C) {
-            uint64_t A[C / 2], B[C / 2];
+            Two A[C / 2], B[C / 2];
             float fa[C], fb[C];
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) {
@@ -506,30 +515,20 @@ bool takes_vectors(const RopeBwdArgs &a, int64_t es, int64_t vb)
     return true;
 }
 
-template <int DT, int VB, int TPR, int NP, int MODE> cudaError_t launch_vec(const RopeBwdArgs &a, BlockSplit *split)
+template <int DT, int VB, int TPR, int NP, int MODE>
+cudaError_t launch_vec(const RopeBwdArgs &a, BlockSplit *split)
 {
     constexpr int G = 32 / TPR, kWarps = kBwdThreads / 32;
     const int64_t most = rope_bwd_max_blocks(a.sm_count) - 2; // blocks on all SMs
-    const int64_t heads = int64_t(a.q_heads) + a.k_heads;
-    auto cut = [&](int64_t h, int *blocks) {
-        Chunks c = {1, 1};
-        *blocks = 0;
-        if (!h)
-            return c;
-        const int64_t steps = (h + G - 1) / G, share = std::max<int64_t>(1, most * h / heads);
-        // The longest chunks (up to ITERS steps) that leave every warp ITEMS of them.
-        int64_t iters = std::min<int64_t>(steps, ITERS);
-        while (iters > 1 && a.tokens * ((steps + iters - 1) / iters) < ITEMS * share * kWarps)
-            iters = (iters + 1) / 2;
-        c.iters = static_cast<uint32_t>(iters);
-        c.per_token = static_cast<uint32_t>((steps + iters - 1) / iters);
-        const int64_t items = a.tokens * c.per_token;
-        *blocks = static_cast<int>(std::max<int64_t>(1, std::min(share, (items + kWarps - 1) / kWarps)));
-        return c;
+    const int64_t qs = (a.q_heads + G - 1) / G, ks = (a.k_heads + G - 1) / G;
+    auto blocks = [&](int64_t steps) { // a step a warp at least
+        const int64_t want = (a.tokens * steps + kWarps - 1) / kWarps;
+        const int64_t share = (most * steps + (qs + ks) / 2) / (qs + ks);
+        return steps ? static_cast<int>(std::max<int64_t>(1, std::min(want, share))) : 0;
     };
-    const Chunks q = cut(a.q_heads, &split->q), k = cut(a.k_heads, &split->k);
+    *split = {blocks(qs), blocks(ks)};
     return launch_kernel(rope_bwd_kernel<DT, VB, TPR, NP, MODE>, split->q + split->k, kBwdThreads,
-                         0, a.base, a, *split, q, k);
+                         0, a.base, a, *split);
 }
 
 template <int DT, int VB, int MODE> cudaError_t launch_lanes(const RopeBwdArgs &a, BlockSplit *split)
@@ -562,7 +561,8 @@ template <int DT, int VB> cudaError_t launch_mode(const RopeBwdArgs &a, BlockSpl
 
 template <int DT> cudaError_t launch_scalar(const RopeBwdArgs &a, BlockSplit *split)
 {
-    const int64_t heads = int64_t(a.q_heads) + a.k_heads, most = 4 * a.sm_count;
+    const int64_t heads = int64_t(a.q_heads) + a.k_heads;
+    const int64_t most = rope_bwd_max_blocks(a.sm_count) - 2;
     auto take = [&](int64_t h) {
         const int64_t want = (a.tokens * h + 7) / 8;
         return h ? std::max<int64_t>(1, std::min(want, (most * h + heads - 1) / heads)) : 0;

@@ -42,7 +42,6 @@ struct Parts {
 // token's angles and the weights are loaded where they are used, once for the
 // U heads of a lane:
 //   y_a = x_a r (g_a cos) - x_b r (g_b sin),  y_b = x_b r (g_b cos) + x_a r (g_a sin)
-// in the packed fp32 form (two IEEE operations an instruction).
 //
 // Memory bounds it once the warps on an SM have enough bytes on the way and
 // few enough instructions between load and store.  Measured (16384 tokens of
@@ -176,7 +175,8 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
 #pragma unroll
             for (int e = 0; e < N; e += C) {
                 // What A r and B r are multiplied by.
-                uint64_t ac[C / 2], as[C / 2], bc[C / 2], bs[C / 2];
+                Two ac[C / 2], as[C / 2], bc[C / 2], bs[C / 2], c[C / 2], s[C / 2];
+                Which on[C / 2];
                 float wa[C], wb[C];
 #pragma unroll
                 for (int i = 0; i < C; ++i)
@@ -191,36 +191,32 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
                     }
                 }
                 couple<C, inter>(ac, bc, wa, wb);
-                uint64_t c[C / 2], s[C / 2], on[C / 2];
                 ld_couples<C, inter>(c, ca, cb, e, on_a, on_b);
                 ld_couples<C, inter>(s, ca + a.rope.rd / 2, cb + a.rope.rd / 2, e, on_a, on_b);
 #pragma unroll
                 for (int i = 0; i < C / 2; ++i) {
-                    // An element without a rotation has 1 and -0 here (x + -0 is
-                    // x, zeros too) and takes 0 for its partner, not 0 times it,
-                    // which could be a NaN.
-                    on[i] = couple_mask<C, inter>(i, on_a, on_b);
-                    const uint64_t one = ~on[i] & f2(1.f, 1.f), nil = ~on[i] & f2(-0.f, -0.f);
-                    as[i] = mul2(ac[i], s[i]) | nil;
-                    bs[i] = neg2(mul2(bc[i], s[i])) | nil;
-                    ac[i] = mul2(ac[i], c[i] | one);
-                    bc[i] = mul2(bc[i], c[i] | one);
+                    // An element without a rotation has 1 and 0 here and takes 0
+                    // for its partner, not 0 times it, which could be a NaN.
+                    on[i] = rotated<C, inter>(i, on_a, on_b);
+                    as[i] = ac[i] * s[i];
+                    bs[i] = bc[i] * s[i];
+                    ac[i] = ac[i] * or_one(c[i], on[i]);
+                    bc[i] = bc[i] * or_one(c[i], on[i]);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 + u * G >= heads)
                         continue; // the whole warp
                     float fa[C], fb[C];
-                    uint64_t A[C / 2], B[C / 2];
+                    Two A[C / 2], B[C / 2];
                     get<DT, VB, C>(fa, x[u][j][0], e);
                     get<DT, VB, C>(fb, x[u][j][1], e);
                     couple<C, inter>(A, B, fa, fb);
-                    const uint64_t r2 = f2(r[u], r[u]);
 #pragma unroll
                     for (int i = 0; i < C / 2; ++i) {
-                        const uint64_t xa = mul2(A[i], r2), xb = mul2(B[i], r2);
-                        A[i] = fma2(xa, ac[i], mul2(xb & on[i], bs[i]));
-                        B[i] = fma2(xb, bc[i], mul2(xa & on[i], as[i]));
+                        const Two xa = A[i] * r[u], xb = B[i] * r[u];
+                        A[i] = fma2(xa, ac[i], -(pick(xb, on[i]) * bs[i]));
+                        B[i] = fma2(xb, bc[i], pick(xa, on[i]) * as[i]);
                     }
                     uncouple<C, inter>(fa, fb, A, B);
                     put<DT, VB, C>(x[u][j][0], e, fa, code, inv);
