@@ -6,9 +6,22 @@
 //
 // Two inputs read and one output written once: memory bounds it.
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 #include "rope.cuh"
 
+#ifdef MAXR
+#define MAXREG __maxnreg__(MAXR)
+#else
+#define MAXREG
+#endif
+#ifndef KEEPMAX
+#define KEEPMAX 16
+#endif
+#ifndef RSTAGES
+#define RSTAGES 3
+#endif
 namespace rmsnorm {
 namespace {
 
@@ -135,19 +148,431 @@ template <int DT> cudaError_t launch_generic(const RmsBwdArgs &a)
     return err;
 }
 
+// ---- rows in registers
+//
+// A group of warps works on a row at a time, every thread on the same
+// columns of each of the group's rows, so that dw's sums stay in registers.
+// With g = w + bias both sums of a row, x^2 and dy g x, are formed at once and
+// meet in shared memory; dx = r (dy g - x r m), m = r sum(dy g x) / hidden.
+//   VEC: 16-byte vectors; each thread copies its own ahead into a ring in
+//        shared memory (cp.async; only its own copies are waited for).
+//   else single elements, for any row length and alignment.
+
+struct RowGroups {
+    int warps;  // of a group
+    int groups; // of a block
+};
+
+template <int DT, int EPT, bool VEC>
+__global__ void __launch_bounds__(512, 1) MAXREG
+rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, float *part,
+                    int64_t rows, int32_t hidden, float bias, float eps, RowGroups rg)
+{
+    using E = Elem<DT>;
+    constexpr int N = VEC ? 16 / E::kSize : 1; // elements of an access
+    constexpr int NV = EPT / N;
+    constexpr int S = VEC ? (NV <= 4 ? RSTAGES : 1) : 0; // ring stages
+    constexpr int kAhead = S > 1 ? S - 1 : 1;
+    // x and dy stay widened in registers between the passes, and so does g; else
+    // they are read again from the ring, and g lies behind it.
+    constexpr bool kKeep = !VEC || EPT <= KEEPMAX;
+    extern __shared__ __align__(16) char ring[];
+    __shared__ float2 sums[2][16];
+    pdl_begin();
+    const int lane = threadIdx.x & 31;
+    const int threads = rg.warps * 32; // of a group
+    const int group = threadIdx.x / threads, t = threadIdx.x - group * threads;
+    const int warp = t >> 5;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * rg.groups;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rg.groups + group;
+    const int nvec = hidden / N;
+    const int64_t row_bytes = static_cast<int64_t>(hidden) * E::kSize;
+    const float inv_n = 1.f / static_cast<float>(hidden);
+
+    auto barrier = [&] { // of the group
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+    };
+    // Sums of two values over the group, in a fixed order.
+    int turn = 0;
+    auto group_sums = [&](float &a, float &b) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, off);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, off);
+        }
+        if (rg.warps == 1)
+            return;
+        // Two sets in turn: a set is written again after a barrier that all
+        // have reached with the set read.
+        float2 *mine = &sums[turn][group * rg.warps];
+        turn ^= 1;
+        if (lane == 0)
+            mine[warp] = make_float2(a, b);
+        barrier();
+        const int from = lane & 15;
+        const float2 v = from < rg.warps ? mine[from] : make_float2(0.f, 0.f);
+        a = v.x, b = v.y;
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, off);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, off);
+        }
+    };
+
+    const uint32_t my = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                        threadIdx.x * 16;
+    const uint32_t step = blockDim.x * 16; // bytes between a thread's vectors
+    // g and dw's sums.
+    Two acc[EPT / 2], g2[kKeep ? EPT / 2 : 1];
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i)
+        acc[i] = two(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = t + j * threads;
+        if constexpr (VEC) {
+            Vec<16> u;
+            vzero(u);
+            if (v < nvec)
+                ld_const(u, w + v * 16);
+            if constexpr (kKeep) {
+                float f[N];
+                get<DT, 16, N>(f, u, 0);
+#pragma unroll
+                for (int i = 0; i < N; i += 2)
+                    g2[(j * N + i) / 2] = two(f[i], f[i + 1]) + bias;
+            } else {
+                st_ring(my + (S * 2 * NV + j) * step, u);
+            }
+        } else if (j % 2 == 0) {
+            g2[j / 2] = two(v < nvec ? E::widen1(w, v) + bias : 0.f,
+                            v + threads < nvec ? E::widen1(w, v + threads) + bias : 0.f);
+        }
+    }
+
+    int64_t next = row0;
+    auto ask_next = [&](int stage) {
+        if constexpr (VEC) {
+            if (next < rows) {
+                const char *px = x + next * row_bytes, *py = dy + next * row_bytes;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int v = t + j * threads;
+                    if (v < nvec) {
+                        const uint32_t p = my + (stage * 2 * NV + 2 * j) * step;
+                        cp_async<16>(p, px + v * 16);
+                        cp_async<16>(p + step, py + v * 16);
+                    }
+                }
+            }
+            next += stride;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+        ask_next(s);
+    int stage = 0;
+    for (int64_t row = row0; row < rows; row += stride) {
+        const uint32_t here = my + stage * 2 * NV * step;
+        Two x2[kKeep ? EPT / 2 : 1], y2[kKeep ? EPT / 2 : 1];
+        if constexpr (VEC) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            if constexpr (S > 1) // into the stage of the row before, whose values are used
+                ask_next(stage == 0 ? S - 1 : stage - 1);
+            stage = stage + 1 >= S ? 0 : stage + 1;
+        } else {
+            const char *px = x + row * row_bytes, *py = dy + row * row_bytes;
+#pragma unroll
+            for (int i = 0; i < EPT; i += 2) {
+                const int c0 = t + i * threads, c1 = c0 + threads;
+                x2[i / 2] = two(c0 < hidden ? E::widen1(px, c0) : 0.f,
+                                c1 < hidden ? E::widen1(px, c1) : 0.f);
+                y2[i / 2] = two(c0 < hidden ? E::widen1(py, c0) : 0.f,
+                                c1 < hidden ? E::widen1(py, c1) : 0.f);
+            }
+        }
+        // Vector j's values, from registers or widened (again): x, dy and g.
+        auto values = [&](int j, Two (&xv)[N > 1 ? N / 2 : 1], Two (&yv)[N > 1 ? N / 2 : 1],
+                          Two (&gv)[N > 1 ? N / 2 : 1], bool first) {
+            if constexpr (!VEC) {
+                xv[0] = x2[j], yv[0] = y2[j], gv[0] = g2[j];
+            } else {
+                const bool in = t + j * threads < nvec;
+                if (first || !kKeep) {
+                    Vec<16> v;
+                    float f[N];
+                    vzero(v);
+                    if (in)
+                        ld_ring(v, here + 2 * j * step);
+                    get<DT, 16, N>(f, v, 0);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i)
+                        xv[i] = two(f[2 * i], f[2 * i + 1]);
+                    vzero(v);
+                    if (in)
+                        ld_ring(v, here + (2 * j + 1) * step);
+                    get<DT, 16, N>(f, v, 0);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i)
+                        yv[i] = two(f[2 * i], f[2 * i + 1]);
+                }
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        const int m = j * (N / 2) + i;
+                        if (first)
+                            x2[m] = xv[i], y2[m] = yv[i];
+                        else
+                            xv[i] = x2[m], yv[i] = y2[m];
+                        gv[i] = g2[m];
+                    }
+                } else {
+                    Vec<16> v;
+                    float f[N];
+                    ld_ring(v, my + (S * 2 * NV + j) * step);
+                    get<DT, 16, N>(f, v, 0);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i)
+                        gv[i] = two(f[2 * i], f[2 * i + 1]) + bias;
+                }
+            }
+        };
+        constexpr int kSteps = VEC ? NV : NV / 2, kHalf = N > 1 ? N / 2 : 1;
+        float sum, dot, k = 1.f;
+        {
+            Two s2 = two(0.f, 0.f), t2 = s2, s3 = s2, t3 = s2;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                Two xv[kHalf], yv[kHalf], gv[kHalf];
+                values(j, xv, yv, gv, true);
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) {
+                    if ((i + j * kHalf) % 2 == 0) {
+                        s2 = fma2(xv[i], xv[i], s2);
+                        t2 = fma2(yv[i] * gv[i], xv[i], t2);
+                    } else {
+                        s3 = fma2(xv[i], xv[i], s3);
+                        t3 = fma2(yv[i] * gv[i], xv[i], t3);
+                    }
+                }
+            }
+            float a0, a1, b0, b1;
+            untwo(s2 + s3, a0, a1);
+            untwo(t2 + t3, b0, b1);
+            sum = a0 + a1;
+            dot = b0 + b1;
+        }
+        group_sums(sum, dot);
+        float r = rsqrtf(fmaf(sum, inv_n, eps));
+        const bool rare = bwd_rescales<DT>(sum, eps); // the same for the group
+        if (rare) {
+            // Again from k x (rope.cuh).
+            k = bwd_rescale_k(sum, eps);
+            sum = dot = 0.f;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                Two xv[kHalf], yv[kHalf], gv[kHalf];
+                values(j, xv, yv, gv, false);
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) {
+                    const Two xk = xv[i] * k;
+                    float a0, a1, b0, b1;
+                    untwo(xk * xk, a0, a1);
+                    untwo(yv[i] * gv[i] * xk, b0, b1);
+                    sum += a0 + a1;
+                    dot += b0 + b1;
+                }
+            }
+            group_sums(sum, dot);
+            r = rsqrtf(fmaf(sum, inv_n, (eps * k) * k));
+        }
+        // xh = x r, dw += dy xh
+        const float m = r * (dot * inv_n);
+        char *po = dx + row * row_bytes;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            Two xv[kHalf], yv[kHalf], gv[kHalf];
+            values(j, xv, yv, gv, false);
+            float f[2 * kHalf];
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+                const Two h = (rare ? xv[i] * k : xv[i]) * r;
+                Two &a = acc[j * kHalf + i];
+                a = fma2(yv[i], h, a);
+                untwo(fma2(h, -m, yv[i] * gv[i]) * r, f[2 * i], f[2 * i + 1]);
+            }
+            if (rare) {
+#pragma unroll
+                for (int i = 0; i < 2 * kHalf; ++i)
+                    f[i] *= k;
+            }
+            if constexpr (VEC) {
+                Vec<16> o;
+                put<DT, 16, N>(o, 0, f);
+                if (t + j * threads < nvec)
+                    st_head(po + (t + j * threads) * 16, o);
+            } else {
+                const int c0 = t + 2 * j * threads, c1 = c0 + threads;
+                if (c0 < hidden)
+                    E::store1(po, c0, f[0]);
+                if (c1 < hidden)
+                    E::store1(po, c1, f[1]);
+            }
+        }
+        if constexpr (VEC && S == 1) {
+            ask_next(0);
+        }
+    }
+    if (!part)
+        return;
+    if constexpr (VEC)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // The block's sums, over its groups in order: each group in turn adds
+    // to shared memory (columns of a thread lie together).
+    float *out = part + static_cast<int64_t>(blockIdx.x) * hidden;
+    float4 *buf = reinterpret_cast<float4 *>(ring) + t; // [EPT / 4][threads]
+    for (int q = 0; q < rg.groups; ++q) {
+        if (rg.groups > 1)
+            __syncthreads();
+        if (group != q)
+            continue;
+#pragma unroll
+        for (int i = 0; i < EPT / 4; ++i) {
+            float4 v;
+            untwo(acc[2 * i], v.x, v.y);
+            untwo(acc[2 * i + 1], v.z, v.w);
+            if (q > 0) {
+                const float4 o = buf[i * threads];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            if (q < rg.groups - 1) {
+                buf[i * threads] = v;
+                continue;
+            }
+            if constexpr (VEC) {
+                const int c = (t + i * 4 / N * threads) * N + i * 4 % N;
+                if (c < hidden)
+                    *reinterpret_cast<float4 *>(out + c) = v;
+            } else {
+                const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t + (4 * i + e) * threads < hidden)
+                        out[t + (4 * i + e) * threads] = f[e];
+            }
+        }
+    }
+}
+
+constexpr int kRowBlocksPerSm = 16; // at most: a workspace row each
+
+// The groups for rows of `accesses` accesses, nv of them a thread.
+RowGroups row_groups(int64_t accesses, int nv)
+{
+    const int warps = static_cast<int>((accesses + 32 * nv - 1) / (32 * nv));
+    return {warps, std::max(1, 8 / warps)};
+}
+
+// Blocks of a kernel that an SM holds, with the kernel's shared memory raised
+// to what it asks; looked up once for a device and launch shape.
+cudaError_t row_occupancy(const void *kernel, int threads, int smem, int *blocks)
+{
+    struct Entry {
+        const void *kernel;
+        int device, threads, smem, blocks;
+    };
+    static std::mutex mu;
+    static std::vector<Entry> known;
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess)
+        return err;
+    std::lock_guard<std::mutex> lk(mu);
+    for (const Entry &e : known)
+        if (e.kernel == kernel && e.device == device && e.threads == threads && e.smem == smem) {
+            *blocks = e.blocks;
+            return cudaSuccess;
+        }
+    int most = smem; // the attribute only grows
+    for (const Entry &e : known)
+        if (e.kernel == kernel && e.device == device)
+            most = std::max(most, e.smem);
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (err == cudaSuccess)
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kernel, threads, smem);
+    if (err != cudaSuccess)
+        return err;
+    if (*blocks < 1)
+        return cudaErrorInvalidConfiguration;
+    known.push_back({kernel, device, threads, smem, *blocks});
+    return cudaSuccess;
+}
+
+template <int DT, int EPT, bool VEC> cudaError_t launch_rows(const RmsBwdArgs &a)
+{
+    constexpr int N = VEC ? 16 / Elem<DT>::kSize : 1;
+    constexpr int NV = EPT / N, S = VEC ? (NV <= 4 ? RSTAGES : 1) : 0;
+    const RowGroups rg = row_groups(a.hidden / N, NV);
+    const int threads = rg.warps * rg.groups * 32;
+    // The ring, and the sums of dw over the groups.
+    constexpr bool keep = !VEC || EPT <= KEEPMAX;
+    const int smem = std::max((S * 2 + (keep ? 0 : 1)) * NV * 16 * threads,
+                              rg.groups > 1 ? rg.warps * 32 * EPT * 4 : 0);
+    auto *kernel = rms_bwd_rows_kernel<DT, EPT, VEC>;
+    int blocks_per_sm = 0;
+    cudaError_t err = row_occupancy(reinterpret_cast<const void *>(kernel), threads, smem,
+                                    &blocks_per_sm);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t want = (a.rows + rg.groups - 1) / rg.groups;
+    const int grid = static_cast<int>(std::min<int64_t>(
+        want, int64_t(std::min(blocks_per_sm, kRowBlocksPerSm)) * a.sm_count));
+    float *part = a.dw ? static_cast<float *>(a.ws) : nullptr;
+    err = launch_kernel(kernel, grid, threads, smem, a.base, static_cast<const char *>(a.dy),
+                        static_cast<const char *>(a.x), static_cast<const char *>(a.w),
+                        static_cast<char *>(a.dx), part, a.rows, static_cast<int32_t>(a.hidden),
+                        a.bias, a.eps, rg);
+    if (err != cudaSuccess || !part)
+        return err;
+    return launch_colsum({part, a.dw, grid, a.hidden, a.hidden}, {}, a.base);
+}
+
+constexpr int64_t kMostRow = 512 * 32; // elements of a row in registers
+
+template <int DT> cudaError_t launch(const RmsBwdArgs &a)
+{
+    const int64_t es = Elem<DT>::kSize;
+    const bool vec = multiple(a.hidden * es, 16) && aligned(a.dy, 16) && aligned(a.x, 16) &&
+                     aligned(a.w, 16) && aligned(a.dx, 16);
+    if (vec && a.hidden <= 512 * 16)
+        return launch_rows<DT, 16, true>(a);
+    if (vec && a.hidden <= kMostRow)
+        return launch_rows<DT, 32, true>(a);
+    if (a.hidden <= 512 * 16)
+        return launch_rows<DT, 16, false>(a);
+    return launch_generic<DT>(a);
+}
+
 } // namespace
 
+// A row of partial sums for every block, or the generic passes' statistics and
+// chunks: whichever is more, for the pointers decide which body runs.
 size_t rms_bwd_workspace(int64_t rows, int64_t hidden, int, int sm_count)
 {
-    return stat_bytes(rows) +
-           static_cast<size_t>(generic_chunks(rows, hidden, sm_count)) * hidden * sizeof(float);
+    const size_t generic = stat_bytes(rows) + static_cast<size_t>(generic_chunks(
+                                                  rows, hidden, sm_count)) *
+                                                  hidden * sizeof(float);
+    const size_t blocks =
+        static_cast<size_t>(std::min<int64_t>(rows, int64_t(kRowBlocksPerSm) * sm_count));
+    return hidden <= kMostRow ? std::max(generic, blocks * hidden * sizeof(float)) : generic;
 }
 
 cudaError_t launch_rms_bwd(const RmsBwdArgs &a, int dtype)
 {
-    return dtype == RMSNORM_F32    ? launch_generic<RMSNORM_F32>(a)
-           : dtype == RMSNORM_BF16 ? launch_generic<RMSNORM_BF16>(a)
-                                   : launch_generic<RMSNORM_F16>(a);
+    return dtype == RMSNORM_F32    ? launch<RMSNORM_F32>(a)
+           : dtype == RMSNORM_BF16 ? launch<RMSNORM_BF16>(a)
+                                   : launch<RMSNORM_F16>(a);
 }
 
 } // namespace rmsnorm

@@ -346,6 +346,39 @@ __device__ inline void put(Vec<VB> &v, int e, const float (&f)[C])
     }
 }
 
+// ---- a lane's own ring of copies
+
+template <int VB> __device__ inline void cp_async(uint32_t dst, const void *src)
+{
+    if constexpr (VB == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(VB)
+                     : "memory");
+}
+template <int VB> __device__ inline void ld_ring(Vec<VB> &v, uint32_t p)
+{
+    if constexpr (VB == 16)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+                     : "r"(p)
+                     : "memory");
+    else if constexpr (VB == 8)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(v.w[0]), "=r"(v.w[1])
+                     : "r"(p)
+                     : "memory");
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.w[0]) : "r"(p) : "memory");
+}
+
+__device__ inline void st_ring(uint32_t p, const Vec<16> &v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v.w[0]), "r"(v.w[1]),
+                 "r"(v.w[2]), "r"(v.w[3])
+                 : "memory");
+}
+
 // ---- host: alignment of a call's tensors
 
 inline bool multiple(int64_t v, int64_t of) { return v % of == 0; }

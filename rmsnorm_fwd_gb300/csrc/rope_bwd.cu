@@ -150,30 +150,6 @@ __global__ void __launch_bounds__(256) rope_bwd_scalar_kernel(const RopeBwdArgs 
 // (96 and 20: 114 us, spills); 3 stages (4: 92.9 us: the larger ring leaves L1 no
 // room for the angles).
 
-template <int VB> __device__ inline void cp_async(uint32_t dst, const void *src)
-{
-    if constexpr (VB == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(VB)
-                     : "memory");
-}
-template <int VB> __device__ inline void ld_ring(Vec<VB> &v, uint32_t p)
-{
-    if constexpr (VB == 16)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
-                     : "r"(p)
-                     : "memory");
-    else if constexpr (VB == 8)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(v.w[0]), "=r"(v.w[1])
-                     : "r"(p)
-                     : "memory");
-    else
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.w[0]) : "r"(p) : "memory");
-}
-
 template <int DT, int VB, int TPR, int NP, int MODE>
 __global__ void __launch_bounds__(kBwdThreads, NP == 1 ? kBwdBlocksPerSm : 1)
 rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
