@@ -11,22 +11,11 @@
 
 #include "rope.cuh"
 
-#ifdef MAXR
-#define MAXREG __maxnreg__(MAXR)
-#else
-#define MAXREG
-#endif
-#ifndef KEEPMAX
-#define KEEPMAX 16
-#endif
-#ifndef RSTAGES
-#define RSTAGES 3
-#endif
 namespace rmsnorm {
 namespace {
 
-// ---- any row length and alignment: statistics, columns, then dx.  Three
-// passes, because a long row does not fit on chip and dx may overwrite dy or
+// ---- rows too long for the registers: statistics, columns, then dx.  Three
+// passes, because such a row does not fit on chip and dx may overwrite dy or
 // x, which the columns' sums still need.
 
 struct RowStat {
@@ -154,28 +143,42 @@ template <int DT> cudaError_t launch_generic(const RmsBwdArgs &a)
 // columns of each of the group's rows, so that dw's sums stay in registers.
 // With g = w + bias both sums of a row, x^2 and dy g x, are formed at once and
 // meet in shared memory; dx = r (dy g - x r m), m = r sum(dy g x) / hidden.
-//   VEC: 16-byte vectors; each thread copies its own ahead into a ring in
-//        shared memory (cp.async; only its own copies are waited for).
-//   else single elements, for any row length and alignment.
+//   VB = 16 or 4: vectors of so many bytes; each thread copies its own ahead into
+//        a ring in shared memory (cp.async; only its own copies are waited for).
+//   VB = 0: single elements, for any row length and alignment.
+//
+// Memory bounds it.  Measured with launch_colsum (16384 x 4096 bf16, 403 MB, floor
+// 60.3 us at the copy bandwidth): three passes 383.9 us; this 65.9 us (6.11 TB/s,
+// 91 %), two blocks of 256 threads on an SM; a ring of two stages 74.9 us; x and
+// dy read again from the ring instead of kept (92 registers for 120) 70.4 us; but
+// 16384 x 5120, where ten warps of 120 registers leave room for one block, 103 us
+// with them kept and 84.7 us (floor 75.3) without.  Capped to 112 registers for a
+// third block of six warps: 34.6 us for 32.9 us (9001 x 2880 f16, floor 23.3).
+// Rows that are no whole vectors: 9001 x 2882 45.5 us with 4-byte vectors, 73.0 us
+// element by element, 183.8 us in three passes.
+
+// Ring stages: as many as leave an SM its blocks (f32 vectors hold half as
+// many values, so a row's take twice the room).
+template <int DT, int EPT, int VB>
+constexpr int kRowStages = VB == 0 ? 0 : Elem<DT>::kSize == 2 ? 3 : EPT <= 16 ? 2 : 1;
 
 struct RowGroups {
     int warps;  // of a group
     int groups; // of a block
 };
 
-template <int DT, int EPT, bool VEC>
-__global__ void __launch_bounds__(512, 1) MAXREG
+template <int DT, int EPT, int VB, bool KEEP>
+__global__ void __launch_bounds__(512, 1)
 rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, float *part,
                     int64_t rows, int32_t hidden, float bias, float eps, RowGroups rg)
 {
     using E = Elem<DT>;
-    constexpr int N = VEC ? 16 / E::kSize : 1; // elements of an access
+    constexpr bool VEC = VB > 0;
+    constexpr int N = VEC ? VB / E::kSize : 1; // elements of an access
     constexpr int NV = EPT / N;
-    constexpr int S = VEC ? (NV <= 4 ? RSTAGES : 1) : 0; // ring stages
+    constexpr int S = kRowStages<DT, EPT, VB>;
     constexpr int kAhead = S > 1 ? S - 1 : 1;
-    // x and dy stay widened in registers between the passes, and so does g; else
-    // they are read again from the ring, and g lies behind it.
-    constexpr bool kKeep = !VEC || EPT <= KEEPMAX;
+    constexpr bool kKeep = KEEP || !VEC;
     extern __shared__ __align__(16) char ring[];
     __shared__ float2 sums[2][16];
     pdl_begin();
@@ -220,8 +223,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     };
 
     const uint32_t my = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
-                        threadIdx.x * 16;
-    const uint32_t step = blockDim.x * 16; // bytes between a thread's vectors
+                        threadIdx.x * VB;
+    const uint32_t step = blockDim.x * VB; // bytes between a thread's vectors
     // g and dw's sums.
     Two acc[EPT / 2], g2[kKeep ? EPT / 2 : 1];
 #pragma unroll
@@ -231,13 +234,13 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     for (int j = 0; j < NV; ++j) {
         const int v = t + j * threads;
         if constexpr (VEC) {
-            Vec<16> u;
+            Vec<VB> u;
             vzero(u);
             if (v < nvec)
-                ld_const(u, w + v * 16);
+                ld_const(u, w + v * VB);
             if constexpr (kKeep) {
                 float f[N];
-                get<DT, 16, N>(f, u, 0);
+                get<DT, VB, N>(f, u, 0);
 #pragma unroll
                 for (int i = 0; i < N; i += 2)
                     g2[(j * N + i) / 2] = two(f[i], f[i + 1]) + bias;
@@ -260,8 +263,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                     const int v = t + j * threads;
                     if (v < nvec) {
                         const uint32_t p = my + (stage * 2 * NV + 2 * j) * step;
-                        cp_async<16>(p, px + v * 16);
-                        cp_async<16>(p + step, py + v * 16);
+                        cp_async<VB>(p, px + v * VB);
+                        cp_async<VB>(p + step, py + v * VB);
                     }
                 }
             }
@@ -300,19 +303,19 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
             } else {
                 const bool in = t + j * threads < nvec;
                 if (first || !kKeep) {
-                    Vec<16> v;
+                    Vec<VB> v;
                     float f[N];
                     vzero(v);
                     if (in)
                         ld_ring(v, here + 2 * j * step);
-                    get<DT, 16, N>(f, v, 0);
+                    get<DT, VB, N>(f, v, 0);
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i)
                         xv[i] = two(f[2 * i], f[2 * i + 1]);
                     vzero(v);
                     if (in)
                         ld_ring(v, here + (2 * j + 1) * step);
-                    get<DT, 16, N>(f, v, 0);
+                    get<DT, VB, N>(f, v, 0);
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i)
                         yv[i] = two(f[2 * i], f[2 * i + 1]);
@@ -328,10 +331,10 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                         gv[i] = g2[m];
                     }
                 } else {
-                    Vec<16> v;
+                    Vec<VB> v;
                     float f[N];
                     ld_ring(v, my + (S * 2 * NV + j) * step);
-                    get<DT, 16, N>(f, v, 0);
+                    get<DT, VB, N>(f, v, 0);
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i)
                         gv[i] = two(f[2 * i], f[2 * i + 1]) + bias;
@@ -408,10 +411,10 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                     f[i] *= k;
             }
             if constexpr (VEC) {
-                Vec<16> o;
-                put<DT, 16, N>(o, 0, f);
+                Vec<VB> o;
+                put<DT, VB, N>(o, 0, f);
                 if (t + j * threads < nvec)
-                    st_head(po + (t + j * threads) * 16, o);
+                    st_head(po + (t + j * threads) * VB, o);
             } else {
                 const int c0 = t + 2 * j * threads, c1 = c0 + threads;
                 if (c0 < hidden)
@@ -450,16 +453,18 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                 buf[i * threads] = v;
                 continue;
             }
-            if constexpr (VEC) {
+            if constexpr (N >= 4) {
                 const int c = (t + i * 4 / N * threads) * N + i * 4 % N;
                 if (c < hidden)
                     *reinterpret_cast<float4 *>(out + c) = v;
             } else {
                 const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t + (4 * i + e) * threads < hidden)
-                        out[t + (4 * i + e) * threads] = f[e];
+                for (int e = 0; e < 4; ++e) {
+                    const int c = (t + (4 * i + e) / N * threads) * N + e % N;
+                    if (c < hidden)
+                        out[c] = f[e];
+                }
             }
         }
     }
@@ -509,17 +514,16 @@ cudaError_t row_occupancy(const void *kernel, int threads, int smem, int *blocks
     return cudaSuccess;
 }
 
-template <int DT, int EPT, bool VEC> cudaError_t launch_rows(const RmsBwdArgs &a)
+template <int DT, int EPT, int VB, bool KEEP> cudaError_t launch_rows(const RmsBwdArgs &a)
 {
-    constexpr int N = VEC ? 16 / Elem<DT>::kSize : 1;
-    constexpr int NV = EPT / N, S = VEC ? (NV <= 4 ? RSTAGES : 1) : 0;
+    constexpr int N = VB ? VB / Elem<DT>::kSize : 1;
+    constexpr int NV = EPT / N, S = kRowStages<DT, EPT, VB>;
     const RowGroups rg = row_groups(a.hidden / N, NV);
     const int threads = rg.warps * rg.groups * 32;
-    // The ring, and the sums of dw over the groups.
-    constexpr bool keep = !VEC || EPT <= KEEPMAX;
-    const int smem = std::max((S * 2 + (keep ? 0 : 1)) * NV * 16 * threads,
+    // The ring (and g), and the sums of dw over the groups.
+    const int smem = std::max((S * 2 + (KEEP ? 0 : 1)) * NV * VB * threads,
                               rg.groups > 1 ? rg.warps * 32 * EPT * 4 : 0);
-    auto *kernel = rms_bwd_rows_kernel<DT, EPT, VEC>;
+    auto *kernel = rms_bwd_rows_kernel<DT, EPT, VB, KEEP>;
     int blocks_per_sm = 0;
     cudaError_t err = row_occupancy(reinterpret_cast<const void *>(kernel), threads, smem,
                                     &blocks_per_sm);
@@ -542,16 +546,53 @@ constexpr int64_t kMostRow = 512 * 32; // elements of a row in registers
 
 template <int DT> cudaError_t launch(const RmsBwdArgs &a)
 {
-    const int64_t es = Elem<DT>::kSize;
-    const bool vec = multiple(a.hidden * es, 16) && aligned(a.dy, 16) && aligned(a.x, 16) &&
-                     aligned(a.w, 16) && aligned(a.dx, 16);
-    if (vec && a.hidden <= 512 * 16)
-        return launch_rows<DT, 16, true>(a);
-    if (vec && a.hidden <= kMostRow)
-        return launch_rows<DT, 32, true>(a);
-    if (a.hidden <= 512 * 16)
-        return launch_rows<DT, 16, false>(a);
-    return launch_generic<DT>(a);
+    constexpr int es = Elem<DT>::kSize;
+    auto fits = [&](int64_t to) {
+        return multiple(a.hidden * es, to) && aligned(a.dy, to) && aligned(a.x, to) &&
+               aligned(a.w, to) && aligned(a.dx, to);
+    };
+    // Short rows: as the heads of one token, several a warp (rope_bwd.cu).  65536
+    // rows of 128: 13.8 us, 26.7 us with a warp a row; of 256: 21.2 us and 27.3 us;
+    // 40000 of 384: 22.5 us and 21.2 us.
+    if (a.hidden <= 256 && a.rows <= (1 << 30) && fits(std::min<int64_t>(16, 2 * es)) &&
+        multiple(a.hidden, 4)) {
+        RopeBwdArgs h{};
+        h.base = a.base;
+        auto view = [&](const void *p) {
+            return HeadsView{static_cast<char *>(const_cast<void *>(p)), a.rows * a.hidden,
+                             a.hidden};
+        };
+        h.qdy = view(a.dy);
+        h.q = view(a.x);
+        h.dq = view(a.dx);
+        h.qw = a.w;
+        h.dqw = a.dw;
+        h.part = a.dw ? static_cast<float *>(a.ws) : nullptr;
+        h.tokens = 1;
+        h.q_heads = static_cast<int32_t>(a.rows);
+        h.head_dim = static_cast<int32_t>(a.hidden);
+        h.bias = a.bias;
+        h.eps = a.eps;
+        h.sm_count = a.sm_count;
+        return launch_rope_bwd(h, DT);
+    }
+    if (fits(16)) {
+        // Ten warps a row: a second block on an SM fits without x and dy kept.
+        if (a.hidden > 9 * 512 && a.hidden <= 10 * 512)
+            return launch_rows<DT, 16, 16, false>(a);
+        if (a.hidden <= 512 * 16)
+            return launch_rows<DT, 16, 16, true>(a);
+        if (a.hidden <= kMostRow)
+            return launch_rows<DT, 32, 16, false>(a);
+        return launch_generic<DT>(a);
+    }
+    if (a.hidden > 512 * 16)
+        return launch_generic<DT>(a);
+    if constexpr (es == 2)
+        if (fits(4))
+            return a.hidden <= 512 ? launch_rows<DT, 4, 4, true>(a)
+                                   : launch_rows<DT, 16, 4, true>(a);
+    return a.hidden <= 512 ? launch_rows<DT, 4, 0, true>(a) : launch_rows<DT, 16, 0, true>(a);
 }
 
 } // namespace

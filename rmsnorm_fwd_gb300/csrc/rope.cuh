@@ -372,6 +372,7 @@ template <int VB> __device__ inline void ld_ring(Vec<VB> &v, uint32_t p)
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.w[0]) : "r"(p) : "memory");
 }
 
+// (16-byte vectors only: what no ring copy brings)
 __device__ inline void st_ring(uint32_t p, const Vec<16> &v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(v.w[0]), "r"(v.w[1]),

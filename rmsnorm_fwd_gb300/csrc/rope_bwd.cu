@@ -570,7 +570,8 @@ template <int DT> cudaError_t launch(const RopeBwdArgs &a)
         return err;
     const int64_t D = a.head_dim;
     return launch_colsum({a.part, a.dqw, split.q, D, D},
-                         {a.part + split.q * D, a.dkw, split.k, D, D}, a.base);
+                         a.dkw ? ColSum{a.part + split.q * D, a.dkw, split.k, D, D} : ColSum{},
+                         a.base);
 }
 
 } // namespace
