@@ -14,6 +14,7 @@ tensors, reads their data pointers and the current stream, and calls
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 
 # element types (rmsnorm_dtype_t)
@@ -135,8 +136,9 @@ def _load() -> ctypes.CDLL:
         vp, i64, i32, f32, u64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                                   ctypes.c_uint64)
         pp = ctypes.POINTER(Plan)
-        hp, rp, szp = (ctypes.POINTER(Heads), ctypes.POINTER(Rope),
-                       ctypes.POINTER(ctypes.c_size_t))
+        # pointers to rmsnorm_heads_t, rmsnorm_rope_t, rmsnorm_paged_cache_t: addresses or byref()
+        hp = rp = cp = vp
+        szp = ctypes.POINTER(ctypes.c_size_t)
         sig = {
             "rmsnorm_create": ([], i32),
             "rmsnorm_destroy": ([], i32),
@@ -165,8 +167,7 @@ def _load() -> ctypes.CDLL:
                                           ctypes.c_size_t, i64, i64, i64, i64, f32, f32, i32,
                                           vp], i32),
             "rmsnorm_qk_norm_rope_bwd_workspace": ([i64, i32, szp], i32),
-            "rmsnorm_qk_norm_rope_append": ([hp, hp, hp, hp, vp, vp, rp,
-                                             ctypes.POINTER(PagedCache), vp, i64, i64, i64, i64,
+            "rmsnorm_qk_norm_rope_append": ([hp, hp, hp, hp, vp, vp, rp, cp, vp, i64, i64, i64, i64,
                                              f32, f32, i32, vp], i32),
             "rmsnorm_bwd": ([vp, vp, vp, vp, vp, vp, ctypes.c_size_t, i64, i64, f32, f32, i32,
                              vp], i32),
@@ -335,15 +336,20 @@ def rmsnorm_validate_plan_epilogue(plan: Plan, x: int, weight: int, y: int, rows
                                                   dtype, epilogue, sm_count, smem_optin)
 
 
+def _ref(structure):
+    return None if structure is None else ctypes.byref(structure)
+
+
 def rmsnorm_qk_norm_rope(q: Heads | None, k: Heads | None, q_out: Heads | None,
                          k_out: Heads | None, q_weight: int, k_weight: int, rope: Rope,
                          tokens: int, q_heads: int, k_heads: int, head_dim: int,
                          weight_bias: float, eps: float, dtype: int,
                          stream: int | None) -> None:
     """Per-head QK norm and position rotation (structures with device pointers)."""
-    _check(_load().rmsnorm_qk_norm_rope(q, k, q_out, k_out, q_weight or None, k_weight or None,
-                                        rope, tokens, q_heads, k_heads, head_dim, weight_bias,
-                                        eps, dtype, stream or None), "rmsnorm_qk_norm_rope")
+    _check(_load().rmsnorm_qk_norm_rope(_ref(q), _ref(k), _ref(q_out), _ref(k_out),
+                                        q_weight or None, k_weight or None, _ref(rope), tokens,
+                                        q_heads, k_heads, head_dim, weight_bias, eps, dtype,
+                                        stream or None), "rmsnorm_qk_norm_rope")
 
 
 def rmsnorm_qk_norm_rope_bwd(dq_out: Heads | None, dk_out: Heads | None, q: Heads | None,
@@ -352,9 +358,10 @@ def rmsnorm_qk_norm_rope_bwd(dq_out: Heads | None, dk_out: Heads | None, q: Head
                              workspace: int, workspace_bytes: int, tokens: int, q_heads: int,
                              k_heads: int, head_dim: int, weight_bias: float, eps: float,
                              dtype: int, stream: int | None) -> None:
-    _check(_load().rmsnorm_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, q_weight or None,
+    _check(_load().rmsnorm_qk_norm_rope_bwd(_ref(dq_out), _ref(dk_out), _ref(q), _ref(k),
+                                            _ref(dq), _ref(dk), q_weight or None,
                                             k_weight or None, dq_weight or None,
-                                            dk_weight or None, rope, workspace or None,
+                                            dk_weight or None, _ref(rope), workspace or None,
                                             workspace_bytes, tokens, q_heads, k_heads, head_dim,
                                             weight_bias, eps, dtype, stream or None),
            "rmsnorm_qk_norm_rope_bwd")
@@ -372,11 +379,11 @@ def rmsnorm_qk_norm_rope_append(q: Heads | None, k: Heads, v: Heads, q_out: Head
                                 slots: int, tokens: int, q_heads: int, k_heads: int,
                                 head_dim: int, weight_bias: float, eps: float, dtype: int,
                                 stream: int | None) -> None:
-    _check(_load().rmsnorm_qk_norm_rope_append(q, k, v, q_out, q_weight or None,
-                                               k_weight or None, rope, cache, slots or None,
-                                               tokens, q_heads, k_heads, head_dim, weight_bias,
-                                               eps, dtype, stream or None),
-           "rmsnorm_qk_norm_rope_append")
+    _check(_load().rmsnorm_qk_norm_rope_append(_ref(q), _ref(k), _ref(v), _ref(q_out),
+                                               q_weight or None, k_weight or None, _ref(rope),
+                                               _ref(cache), slots or None, tokens, q_heads,
+                                               k_heads, head_dim, weight_bias, eps, dtype,
+                                               stream or None), "rmsnorm_qk_norm_rope_append")
 
 
 def rmsnorm_bwd(dy: int, x: int, weight: int, dx: int, dweight: int, workspace: int,
@@ -644,66 +651,103 @@ def _check_rows(x, weight):
         raise ValueError("weight must have hidden elements")
 
 
+# The structures of a call as bytes: ctypes hands the library their address
+# (read during the call only), at a third of the time that building ctypes
+# structures takes, which a decode step would notice.
+_HEADS = struct.Struct("@Pqq")          # rmsnorm_heads_t
+_ROPE = struct.Struct("@PPqii")         # rmsnorm_rope_t
+_CACHE = struct.Struct("@PPqqqqqiff0q")  # rmsnorm_paged_cache_t, padded to its end
+
+
 def _launch_on(device, stream, call):
     """call(raw stream) with `device` current, on `stream` or the device's
     current stream.  Tensors made in `call` belong to that stream."""
     import torch
-    ensure_context(device.index)
+    if device.index not in _created:
+        ensure_context(device.index)
     if stream is not None:
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
+    raw = torch._C._cuda_getCurrentRawStream
     if torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream(device).cuda_stream)
+        return call(raw(device.index))
     with torch.cuda.device(device):
-        return call(torch.cuda.current_stream(device).cuda_stream)
+        return call(raw(device.index))
 
 
-def _heads_of(t, name: str, like=None):
+_sms: dict[int, int] = {}
+
+
+def _sm_count(index: int) -> int:
+    """SM count of the current device, `index` (one that has a context)."""
+    n = _sms.get(index)
+    if n is None:
+        n = _sms[index] = rmsnorm_device_limits()[0]
+    return n
+
+
+def _heads(t, name: str, like=None) -> tuple[bytes, int]:
     """(rmsnorm_heads_t, tokens) of a CUDA tensor [..., heads, head_dim] whose
     leading dimensions step evenly over the tokens."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     shape, strides = t.shape, t.stride()
-    if len(shape) < 3:
-        raise ValueError(f"{name} must be [..., tokens, heads, head_dim]")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise TypeError(f"{name} must have the dtype and device of the other tensors")
-    if shape[-1] > 1 and strides[-1] != 1:
+    if len(shape) == 3:
+        tokens, heads, dim = shape
+        step, head_step, last = strides
+        if tokens == 1:
+            step = 0
+    elif len(shape) > 3:
+        heads, dim = shape[-2:]
+        head_step, last = strides[-2:]
+        tokens, step = 1, 0
+        for n, s in zip(shape[-3::-1], strides[-3::-1]):
+            if n != 1:
+                if tokens == 1:
+                    step = s
+                elif s != step * tokens:
+                    raise ValueError(f"the leading dimensions of {name} must step evenly")
+                tokens *= n
+    else:
+        raise ValueError(f"{name} must be [..., tokens, heads, head_dim]")
+    if dim > 1 and last != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    tokens, step = 1, 0
-    for n, s in zip(shape[-3::-1], strides[-3::-1]):
-        if n != 1:
-            if tokens == 1:
-                step = s
-            elif s != step * tokens:
-                raise ValueError(f"the leading dimensions of {name} must step evenly")
-            tokens *= n
-    heads = shape[-2]
-    if t.numel() and ((tokens > 1 and step == 0) or (heads > 1 and strides[-2] == 0)):
+    if heads == 1:
+        head_step = 0
+    elif head_step == 0 or (tokens > 1 and step == 0):
         raise ValueError(f"{name} must not be an expanded tensor")
-    return Heads(t.data_ptr(), step, strides[-2] if heads > 1 else 0), tokens
+    if tokens > 1 and step == 0:
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return _HEADS.pack(t.data_ptr(), step, head_step), tokens
 
 
-def _rope_of(cos_sin, positions, tokens: int, interleaved: bool, device) -> Rope:
+_NO_ROPE = _ROPE.pack(0, 0, 0, 0, 0)
+
+
+def _rope(cos_sin, positions, tokens: int, interleaved: bool, device) -> bytes:
+    """The rmsnorm_rope_t."""
     import torch
     if cos_sin is None:
-        return Rope(None, None, 0, 0, 0)
+        return _NO_ROPE
     if cos_sin.dtype != torch.float32 or positions.dtype != torch.int64:
         raise TypeError("cos_sin must be float32 and positions int64")
     if cos_sin.device != device or positions.device != device:
         raise ValueError("cos_sin and positions must be on the device of q and k")
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or not positions.is_contiguous():
+    shape = cos_sin.shape
+    if len(shape) != 2 or not cos_sin.is_contiguous() or not positions.is_contiguous():
         raise ValueError("cos_sin must be [max_position, rotary_dim], cos_sin and positions "
                          "contiguous")
     if positions.numel() != tokens:
         raise ValueError("positions must hold one position for each token")
-    return Rope(cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-                1 if interleaved else 0)
+    return _ROPE.pack(cos_sin.data_ptr(), positions.data_ptr(), shape[0], shape[1],
+                      1 if interleaved else 0)
 
 
-def _head_weight(w, name: str, like) -> int:
+def _head_weight(w, name: str, like):
     if w is None:
-        return 0
+        return None
     if w.dtype != like.dtype or w.device != like.device:
         raise TypeError(f"{name} must have the dtype and device of its heads")
     if w.numel() != like.shape[-1] or not w.is_contiguous():
@@ -731,23 +775,30 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
     A position outside the table leaves its token out and is reported by
     rmsnorm_get_device_status (ERR_BAD_INDEX).  Runs on ``stream`` (default:
     PyTorch's current stream)."""
-    qh, tokens = _heads_of(q, "q")
-    kh, k_tokens = (None, tokens) if k is None else _heads_of(k, "k", q)
-    if k_tokens != tokens or (k is not None and k.shape[-1] != q.shape[-1]):
-        raise ValueError("q and k must hold the same number of tokens and one head_dim")
+    qh, tokens = _heads(q, "q")
+    head_dim = q.shape[-1]
+    kh, k_heads = None, 0
+    if k is not None:
+        kh, k_tokens = _heads(k, "k", q)
+        k_heads = k.shape[-2]
+        if k_tokens != tokens or k.shape[-1] != head_dim:
+            raise ValueError("q and k must hold the same number of tokens and one head_dim")
     qo = ko = None
     if q_out is not None:
         _same_shape(q_out, q, "q_out")
-        qo = _heads_of(q_out, "q_out", q)[0]
+        qo = _heads(q_out, "q_out", q)[0]
     if k_out is not None:
+        if k is None:
+            raise ValueError("k_out without k")
         _same_shape(k_out, k, "k_out")
-        ko = _heads_of(k_out, "k_out", q)[0]
-    rope = _rope_of(cos_sin, positions, tokens, interleaved, q.device)
+        ko = _heads(k_out, "k_out", q)[0]
+    rope = _rope(cos_sin, positions, tokens, interleaved, q.device)
     qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
-    k_heads = 0 if k is None else k.shape[-2]
-    _launch_on(q.device, stream, lambda s: rmsnorm_qk_norm_rope(
-        qh, kh, qo, ko, qw, kw, rope, tokens, q.shape[-2], k_heads, q.shape[-1], weight_bias, eps,
-        torch_dtype_code(q.dtype), s))
+    code = torch_dtype_code(q.dtype)
+    fn = _load().rmsnorm_qk_norm_rope
+    _check(_launch_on(q.device, stream, lambda s: fn(
+        qh, kh, qo, ko, qw, kw, rope, tokens, q.shape[-2], k_heads, head_dim, weight_bias, eps,
+        code, s)), "rmsnorm_qk_norm_rope")
     return q if q_out is None else q_out, k if k_out is None else k_out
 
 
@@ -762,43 +813,50 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     float32 [head_dim] (None with ``weight_grads=False``).  k and dk_out may
     be None.  Other arguments as for ``qk_norm_rope``."""
     import torch
-    qh, tokens = _heads_of(q, "q")
-    kh, k_tokens = (None, tokens) if k is None else _heads_of(k, "k", q)
-    if k_tokens != tokens or (k is not None and k.shape[-1] != q.shape[-1]):
-        raise ValueError("q and k must hold the same number of tokens and one head_dim")
+    qh, tokens = _heads(q, "q")
+    head_dim = q.shape[-1]
     _same_shape(dq_out, q, "dq_out")
-    qy, ky = _heads_of(dq_out, "dq_out", q)[0], None
+    qy = _heads(dq_out, "dq_out", q)[0]
+    if dq is not None:
+        _same_shape(dq, q, "dq")
+    kh = ky = None
+    k_heads = 0
     if k is not None:
+        kh, k_tokens = _heads(k, "k", q)
+        k_heads = k.shape[-2]
+        if k_tokens != tokens or k.shape[-1] != head_dim:
+            raise ValueError("q and k must hold the same number of tokens and one head_dim")
         _same_shape(dk_out, k, "dk_out")
-        ky = _heads_of(dk_out, "dk_out", q)[0]
-    rope = _rope_of(cos_sin, positions, tokens, interleaved, q.device)
+        ky = _heads(dk_out, "dk_out", q)[0]
+        if dk is not None:
+            _same_shape(dk, k, "dk")
+    rope = _rope(cos_sin, positions, tokens, interleaved, q.device)
     qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
-    head_dim, k_heads = q.shape[-1], 0 if k is None else k.shape[-2]
+    code = torch_dtype_code(q.dtype)
+    fn = _load().rmsnorm_qk_norm_rope_bwd
+    device = q.device
 
     def call(s):
-        q_grad = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        _same_shape(q_grad, q, "dq")
-        k_grad = dk
+        q_grad = torch.empty(q.shape, dtype=q.dtype, device=device) if dq is None else dq
+        qd, kd, k_grad = _heads(q_grad, "dq", q)[0], None, dk
         if k is not None:
             if k_grad is None:
-                k_grad = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-            _same_shape(k_grad, k, "dk")
-        w_grads = ws = None
+                k_grad = torch.empty(k.shape, dtype=q.dtype, device=device)
+            kd = _heads(k_grad, "dk", q)[0]
+        p = wp = None
+        need = 0
+        qg = kg = None
         if weight_grads:
-            need = rmsnorm_qk_norm_rope_bwd_workspace(head_dim, rmsnorm_device_limits()[0])
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            w_grads = torch.empty(2, head_dim, dtype=torch.float32, device=q.device)
-        p = w_grads.data_ptr() if weight_grads else 0
-        rmsnorm_qk_norm_rope_bwd(qy, ky, qh, kh, _heads_of(q_grad, "dq", q)[0],
-                                 None if k is None else _heads_of(k_grad, "dk", q)[0], qw, kw, p,
-                                 p + 4 * head_dim if p else 0, rope, ws.data_ptr() if p else 0,
-                                 ws.numel() if p else 0, tokens, q.shape[-2], k_heads, head_dim,
-                                 weight_bias, eps, torch_dtype_code(q.dtype), s)
-        if not weight_grads:
-            return q_grad, k_grad, None, None
-        return q_grad, k_grad, w_grads[0], w_grads[1]
+            need = rmsnorm_qk_norm_rope_bwd_workspace(head_dim, _sm_count(device.index))
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            qg, kg = torch.empty(2, head_dim, dtype=torch.float32, device=device).unbind()
+            wp, p = ws.data_ptr(), qg.data_ptr()
+        _check(fn(qy, ky, qh, kh, qd, kd, qw, kw, p, p and p + 4 * head_dim, rope, wp, need,
+                  tokens, q.shape[-2], k_heads, head_dim, weight_bias, eps, code, s),
+               "rmsnorm_qk_norm_rope_bwd")
+        return q_grad, k_grad, qg, kg
 
-    return _launch_on(q.device, stream, call)
+    return _launch_on(device, stream, call)
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, k_cache, v_cache,
@@ -811,48 +869,54 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
     slots[t] = page * page_size + slot.  Returns q_out.
 
     ``slots``: int64, one for each token; a negative one marks padding, of
-    which nothing is written and whose values have no effect; the others must
-    differ.  Caches hold the
-    elements' dtype, or E4M3 codes of value / scale (float8_e4m3fn or uint8).
-    Weights None: the rotation alone.  k and v are left as they were; ``q`` may
-    be None."""
+    which nothing is written and whose values and position have no effect; the
+    others must differ.  Caches hold the elements' dtype, or E4M3 codes of
+    value / scale (float8_e4m3fn or uint8).  Weights None: the rotation alone.
+    k and v are left as they were; ``q`` may be None."""
     import torch
-    kh, tokens = _heads_of(k, "k")
-    vh, v_tokens = _heads_of(v, "v", k)
-    qh, q_tokens = (None, tokens) if q is None else _heads_of(q, "q", k)
-    if v.shape[-2:] != k.shape[-2:] or v_tokens != tokens or q_tokens != tokens or \
-            (q is not None and q.shape[-1] != k.shape[-1]):
-        raise ValueError("q, k and v must hold the same number of tokens and one head_dim, k and "
-                         "v the same heads")
-    qo = None
+    kh, tokens = _heads(k, "k")
+    vh, v_tokens = _heads(v, "v", k)
+    k_heads, head_dim = k.shape[-2:]
+    qh, q_heads, q_tokens, qo = None, 0, tokens, None
+    if q is not None:
+        qh, q_tokens = _heads(q, "q", k)
+        q_heads = q.shape[-2]
+        if q.shape[-1] != head_dim:
+            raise ValueError("q and k must hold one head_dim")
+    if v.shape[-2:] != k.shape[-2:] or v_tokens != tokens or q_tokens != tokens:
+        raise ValueError("q, k and v must hold the same number of tokens, k and v the same heads")
     if q_out is not None:
+        if q is None:
+            raise ValueError("q_out without q")
         _same_shape(q_out, q, "q_out")
-        qo = _heads_of(q_out, "q_out", k)[0]
+        qo = _heads(q_out, "q_out", k)[0]
+    device = k.device
     if slots.dtype != torch.int64:
         raise TypeError("slots must be int64")
-    if slots.device != k.device or slots.numel() != tokens or not slots.is_contiguous():
+    if slots.device != device or slots.numel() != tokens or not slots.is_contiguous():
         raise ValueError("slots must be contiguous, one for each token, on the device of k")
-    k_heads, head_dim = k.shape[-2], k.shape[-1]
-    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[-2:] or \
-            v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != k_heads or shape[3] != head_dim or \
+            v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, head_dim] with "
                          "the same strides")
-    if k_cache.dtype != v_cache.dtype or k_cache.device != k.device or v_cache.device != k.device:
+    dtype = k_cache.dtype
+    if v_cache.dtype != dtype or k_cache.device != device or v_cache.device != device:
         raise TypeError("k_cache and v_cache must have one dtype and the device of k")
-    st = k_cache.stride()
     if head_dim > 1 and st[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
-    e4m3 = k_cache.dtype in (torch.float8_e4m3fn, torch.uint8)
-    if not e4m3 and k_cache.dtype != k.dtype:
+    e4m3 = dtype != k.dtype
+    if e4m3 and dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError("the caches must hold the dtype of k, float8_e4m3fn or uint8")
-    cache = PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1],
-                       st[0], st[1], st[2], 1 if e4m3 else 0, k_scale, v_scale)
-    rope = _rope_of(cos_sin, positions, tokens, interleaved, k.device)
+    cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], st[0], st[1],
+                        st[2], e4m3, k_scale, v_scale)
+    rope = _rope(cos_sin, positions, tokens, interleaved, device)
     qw, kw = _head_weight(q_weight, "q_weight", k), _head_weight(k_weight, "k_weight", k)
-    q_heads = 0 if q is None else q.shape[-2]
-    _launch_on(k.device, stream, lambda s: rmsnorm_qk_norm_rope_append(
+    code = torch_dtype_code(k.dtype)
+    fn = _load().rmsnorm_qk_norm_rope_append
+    _check(_launch_on(device, stream, lambda s: fn(
         qh, kh, vh, qo, qw, kw, rope, cache, slots.data_ptr(), tokens, q_heads, k_heads, head_dim,
-        weight_bias, eps, torch_dtype_code(k.dtype), s))
+        weight_bias, eps, code, s)), "rmsnorm_qk_norm_rope_append")
     return q if q_out is None else q_out
 
 
@@ -865,11 +929,12 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
     ``weight_grad=False``)."""
     import torch
     _check_rows(x, weight)
+    device = x.device
     for t, name in ((dy, "dy"), (dx, "dx")):
         if t is not None and (t.shape != x.shape or t.dtype != x.dtype or
-                              t.device != x.device or not t.is_contiguous()):
+                              t.device != device or not t.is_contiguous()):
             raise ValueError(f"{name} must match x (shape, dtype, device, contiguous)")
-    if weight.device != x.device:
+    if weight.device != device:
         raise ValueError("weight must be on the device of x")
     hidden = x.shape[-1]
     rows = x.numel() // hidden if hidden else 0
@@ -877,12 +942,12 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
 
     def call(s):
         grad = torch.empty_like(x) if dx is None else dx
-        need = rmsnorm_bwd_workspace(rows, hidden, code, rmsnorm_device_limits()[0])
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        w_grad = torch.empty(hidden, dtype=torch.float32, device=x.device) if weight_grad else None
+        need = rmsnorm_bwd_workspace(rows, hidden, code, _sm_count(device.index))
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        w_grad = torch.empty(hidden, dtype=torch.float32, device=device) if weight_grad else None
         rmsnorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), grad.data_ptr(),
                     w_grad.data_ptr() if weight_grad else 0, ws.data_ptr(), need, rows, hidden,
                     weight_bias, eps, code, s)
         return grad, w_grad
 
-    return _launch_on(x.device, stream, call)
+    return _launch_on(device, stream, call)

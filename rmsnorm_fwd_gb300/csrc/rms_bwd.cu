@@ -470,14 +470,16 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     }
 }
 
-constexpr int kRowBlocksPerSm = 16; // at most: a workspace row each
-
 // The groups for rows of `accesses` accesses, nv of them a thread.
 RowGroups row_groups(int64_t accesses, int nv)
 {
     const int warps = static_cast<int>((accesses + 32 * nv - 1) / (32 * nv));
     return {warps, std::max(1, 8 / warps)};
 }
+
+// Blocks on an SM, a workspace row each: no more than 1024 threads (the bodies
+// have 61 registers and more, 64 as they are given out).
+int row_blocks(const RowGroups &rg) { return std::max(1, 32 / (rg.warps * rg.groups)); }
 
 // Blocks of a kernel that an SM holds, with the kernel's shared memory raised
 // to what it asks; looked up once for a device and launch shape.
@@ -531,7 +533,7 @@ template <int DT, int EPT, int VB, bool KEEP> cudaError_t launch_rows(const RmsB
         return err;
     const int64_t want = (a.rows + rg.groups - 1) / rg.groups;
     const int grid = static_cast<int>(std::min<int64_t>(
-        want, int64_t(std::min(blocks_per_sm, kRowBlocksPerSm)) * a.sm_count));
+        want, int64_t(std::min(blocks_per_sm, row_blocks(rg))) * a.sm_count));
     float *part = a.dw ? static_cast<float *>(a.ws) : nullptr;
     err = launch_kernel(kernel, grid, threads, smem, a.base, static_cast<const char *>(a.dy),
                         static_cast<const char *>(a.x), static_cast<const char *>(a.w),
@@ -543,6 +545,7 @@ template <int DT, int EPT, int VB, bool KEEP> cudaError_t launch_rows(const RmsB
 }
 
 constexpr int64_t kMostRow = 512 * 32; // elements of a row in registers
+constexpr int64_t kHeadRow = 256;      // of one that goes as a head
 
 template <int DT> cudaError_t launch(const RmsBwdArgs &a)
 {
@@ -554,7 +557,7 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
     // Short rows: as the heads of one token, several a warp (rope_bwd.cu).  65536
     // rows of 128: 13.8 us, 26.7 us with a warp a row; of 256: 21.2 us and 27.3 us;
     // 40000 of 384: 22.5 us and 21.2 us.
-    if (a.hidden <= 256 && a.rows <= (1 << 30) && fits(std::min<int64_t>(16, 2 * es)) &&
+    if (a.hidden <= kHeadRow && a.rows <= (1 << 30) && fits(std::min<int64_t>(16, 2 * es)) &&
         multiple(a.hidden, 4)) {
         RopeBwdArgs h{};
         h.base = a.base;
@@ -597,16 +600,21 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
 
 } // namespace
 
-// A row of partial sums for every block, or the generic passes' statistics and
-// chunks: whichever is more, for the pointers decide which body runs.
+// A row of partial sums for every block of any body that may run (the pointers
+// decide which), or the three passes' statistics and chunks.
 size_t rms_bwd_workspace(int64_t rows, int64_t hidden, int, int sm_count)
 {
-    const size_t generic = stat_bytes(rows) + static_cast<size_t>(generic_chunks(
-                                                  rows, hidden, sm_count)) *
-                                                  hidden * sizeof(float);
-    const size_t blocks =
-        static_cast<size_t>(std::min<int64_t>(rows, int64_t(kRowBlocksPerSm) * sm_count));
-    return hidden <= kMostRow ? std::max(generic, blocks * hidden * sizeof(float)) : generic;
+    const size_t row = static_cast<size_t>(hidden) * sizeof(float);
+    size_t blocks = 0;
+    for (int ept : {4, 16, 32})
+        if (hidden <= 512 * ept)
+            blocks = std::max(blocks, static_cast<size_t>(row_blocks(row_groups(hidden, ept))) *
+                                          sm_count);
+    if (hidden <= kHeadRow)
+        blocks = std::max(blocks, static_cast<size_t>(rope_bwd_max_blocks(sm_count)));
+    blocks = std::min(blocks, static_cast<size_t>(rows));
+    const size_t passes = stat_bytes(rows) + generic_chunks(rows, hidden, sm_count) * row;
+    return hidden <= 512 * 16 ? blocks * row : std::max(blocks * row, passes);
 }
 
 cudaError_t launch_rms_bwd(const RmsBwdArgs &a, int dtype)

@@ -1,5 +1,6 @@
 """Argument checks of the rotation, cache and gradient entry points, without a
 GPU: pointers are numbers that no check follows."""
+import ctypes
 import itertools
 import random
 
@@ -30,8 +31,9 @@ def H(data, ts=0, hs=0):
 
 def fwd(q=H(ptr(0)), k=H(ptr(1)), qo=None, ko=None, qw=ptr(10), kw=ptr(11), rp=None, T=4, hq=8,
         hk=2, D=128, bias=0.0, eps=1e-6, dtype=rn.BF16):
-    return rn._load().rmsnorm_qk_norm_rope(q, k, qo, ko, qw, kw, rp or rope(), T, hq, hk, D, bias,
-                                           eps, dtype, None)
+    return rn._load().rmsnorm_qk_norm_rope(*map(rn._ref, (q, k, qo, ko)), qw, kw,
+                                           rn._ref(rp or rope()), T, hq, hk, D, bias, eps, dtype,
+                                           None)
 
 
 SIZES = [
@@ -123,9 +125,9 @@ def test_overlap_rule_against_brute_force():
 def bwd(qy=H(ptr(0)), ky=H(ptr(1)), q=H(ptr(2)), k=H(ptr(3)), dq=H(ptr(4)), dk=H(ptr(5)),
         qw=ptr(10), kw=ptr(11), dqw=ptr(12), dkw=ptr(13), rp=None, ws=ptr(14), wb=1 << 30, T=4,
         hq=8, hk=2, D=128, bias=0.0, eps=1e-6, dtype=rn.BF16):
-    return rn._load().rmsnorm_qk_norm_rope_bwd(qy, ky, q, k, dq, dk, qw, kw, dqw, dkw,
-                                               rp or rope(), ws, wb, T, hq, hk, D, bias, eps,
-                                               dtype, None)
+    return rn._load().rmsnorm_qk_norm_rope_bwd(*map(rn._ref, (qy, ky, q, k, dq, dk)), qw, kw, dqw,
+                                               dkw, rn._ref(rp or rope()), ws, wb, T, hq, hk, D,
+                                               bias, eps, dtype, None)
 
 
 def test_gradient_arguments():
@@ -169,7 +171,8 @@ def cache(**kw):
 
 def append(q=H(ptr(0)), k=H(ptr(1)), v=H(ptr(2)), qo=None, qw=ptr(10), kw=ptr(11), rp=None,
            c=None, slots=ptr(17), T=4, hq=8, hk=2, D=128, bias=0.0, eps=1e-6, dtype=rn.BF16):
-    return rn._load().rmsnorm_qk_norm_rope_append(q, k, v, qo, qw, kw, rp or rope(), c or cache(),
+    return rn._load().rmsnorm_qk_norm_rope_append(*map(rn._ref, (q, k, v, qo)), qw, kw,
+                                                  rn._ref(rp or rope()), rn._ref(c or cache()),
                                                   slots, T, hq, hk, D, bias, eps, dtype, None)
 
 
@@ -274,8 +277,22 @@ class Fake:
         return P
 
 
+def test_packed_structures_are_the_structures():
+    h = rn.Heads.from_buffer_copy(rn._HEADS.pack(1, 2, 3))
+    assert (h.data, h.token_stride, h.head_stride) == (1, 2, 3)
+    r = rn.Rope.from_buffer_copy(rn._ROPE.pack(1, 2, 3, 4, 5))
+    assert [getattr(r, n) for n, _ in r._fields_] == [1, 2, 3, 4, 5]
+    c = rn.PagedCache.from_buffer_copy(rn._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 1, 0.5, 0.25))
+    assert [getattr(c, n) for n, _ in c._fields_] == [1, 2, 3, 4, 5, 6, 7, 1, 0.5, 0.25]
+    for packed, whole in ((rn._HEADS, rn.Heads), (rn._ROPE, rn.Rope), (rn._CACHE, rn.PagedCache)):
+        assert packed.size == ctypes.sizeof(whole)
+
+
 def test_layouts_of_tensors():
-    of = lambda shape, strides: rn._heads_of(Fake(shape, strides), "q")
+    def of(shape, strides):
+        packed, tokens = rn._heads(Fake(shape, strides), "q")
+        return rn.Heads.from_buffer_copy(packed), tokens
+
     h, n = of((5, 8, 64), (512, 64, 1))
     assert (h.token_stride, h.head_stride, n) == (512, 64, 5)
     h, n = of((2, 5, 8, 64), (5 * 900, 900, 64, 1))
