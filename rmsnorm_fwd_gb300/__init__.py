@@ -843,17 +843,16 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
             if k_grad is None:
                 k_grad = torch.empty(k.shape, dtype=q.dtype, device=device)
             kd = _heads(k_grad, "dk", q)[0]
-        p = wp = None
+        wp = qp = kp = qg = kg = None
         need = 0
-        qg = kg = None
         if weight_grads:
             need = rmsnorm_qk_norm_rope_bwd_workspace(head_dim, _sm_count(device.index))
             ws = torch.empty(need, dtype=torch.uint8, device=device)
-            qg, kg = torch.empty(2, head_dim, dtype=torch.float32, device=device).unbind()
-            wp, p = ws.data_ptr(), qg.data_ptr()
-        _check(fn(qy, ky, qh, kh, qd, kd, qw, kw, p, p and p + 4 * head_dim, rope, wp, need,
-                  tokens, q.shape[-2], k_heads, head_dim, weight_bias, eps, code, s),
-               "rmsnorm_qk_norm_rope_bwd")
+            qg = torch.empty(head_dim, dtype=torch.float32, device=device)
+            kg = torch.empty(head_dim, dtype=torch.float32, device=device)
+            wp, qp, kp = ws.data_ptr(), qg.data_ptr(), kg.data_ptr()
+        _check(fn(qy, ky, qh, kh, qd, kd, qw, kw, qp, kp, rope, wp, need, tokens, q.shape[-2],
+                  k_heads, head_dim, weight_bias, eps, code, s), "rmsnorm_qk_norm_rope_bwd")
         return q_grad, k_grad, qg, kg
 
     return _launch_on(device, stream, call)
@@ -939,15 +938,16 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
     hidden = x.shape[-1]
     rows = x.numel() // hidden if hidden else 0
     code = torch_dtype_code(x.dtype)
+    fn = _load().rmsnorm_bwd
 
     def call(s):
         grad = torch.empty_like(x) if dx is None else dx
         need = rmsnorm_bwd_workspace(rows, hidden, code, _sm_count(device.index))
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         w_grad = torch.empty(hidden, dtype=torch.float32, device=device) if weight_grad else None
-        rmsnorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), grad.data_ptr(),
-                    w_grad.data_ptr() if weight_grad else 0, ws.data_ptr(), need, rows, hidden,
-                    weight_bias, eps, code, s)
+        _check(fn(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), grad.data_ptr(),
+                  w_grad.data_ptr() if weight_grad else None, ws.data_ptr(), need, rows, hidden,
+                  weight_bias, eps, code, s), "rmsnorm_bwd")
         return grad, w_grad
 
     return _launch_on(device, stream, call)

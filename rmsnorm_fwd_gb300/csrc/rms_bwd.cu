@@ -7,7 +7,6 @@
 // Two inputs read and one output written once: memory bounds it.
 #include <algorithm>
 #include <mutex>
-#include <vector>
 
 #include "rope.cuh"
 
@@ -482,29 +481,33 @@ RowGroups row_groups(int64_t accesses, int nv)
 int row_blocks(const RowGroups &rg) { return std::max(1, 32 / (rg.warps * rg.groups)); }
 
 // Blocks of a kernel that an SM holds, with the kernel's shared memory raised
-// to what it asks; looked up once for a device and launch shape.
+// to what it asks; remembered for a device and launch shape.
 cudaError_t row_occupancy(const void *kernel, int threads, int smem, int *blocks)
 {
     struct Entry {
         const void *kernel;
         int device, threads, smem, blocks;
     };
+    constexpr int kMost = 256;
     static std::mutex mu;
-    static std::vector<Entry> known;
+    static Entry known[kMost];
+    static int count = 0;
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess)
         return err;
     std::lock_guard<std::mutex> lk(mu);
-    for (const Entry &e : known)
-        if (e.kernel == kernel && e.device == device && e.threads == threads && e.smem == smem) {
+    int most = smem; // the attribute only grows
+    for (int i = 0; i < count; ++i) {
+        const Entry &e = known[i];
+        if (e.kernel != kernel || e.device != device)
+            continue;
+        if (e.threads == threads && e.smem == smem) {
             *blocks = e.blocks;
             return cudaSuccess;
         }
-    int most = smem; // the attribute only grows
-    for (const Entry &e : known)
-        if (e.kernel == kernel && e.device == device)
-            most = std::max(most, e.smem);
+        most = std::max(most, e.smem);
+    }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (err == cudaSuccess)
         err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kernel, threads, smem);
@@ -512,7 +515,8 @@ cudaError_t row_occupancy(const void *kernel, int threads, int smem, int *blocks
         return err;
     if (*blocks < 1)
         return cudaErrorInvalidConfiguration;
-    known.push_back({kernel, device, threads, smem, *blocks});
+    if (count < kMost)
+        known[count++] = {kernel, device, threads, smem, *blocks};
     return cudaSuccess;
 }
 

@@ -95,26 +95,64 @@ def test_many_rows(rows, hidden):
     assert torch.equal(rn.rms_norm_backward(dy, x, w, 1e-5)[1], dw)
 
 
-@pytest.mark.parametrize("hidden", [128, 1024, 4096, 5000, 16384, 40000])
+@pytest.mark.parametrize("hidden", [100, 128, 131, 1024, 1027, 4096, 5000, 5120, 16384, 40000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_extreme_rows(dtype, hidden):
-    dy, x, w, _ = make(dtype, 12, hidden, 4)
+    dy, x, w, _ = make(dtype, 20, hidden, 4)
     dt = R.DT[dtype]
     big, small = ((2.0 ** 100, 2.0 ** -110) if dtype != "f16" else (2.0 ** 11, 2.0 ** -14))
-    scale = torch.ones(12, 1, dtype=torch.float64, device="cuda")
+    scale = torch.ones(20, 1, dtype=torch.float64, device="cuda")
     scale[1], scale[2], scale[3], scale[4] = big, small, 0.0, big * 2.0 ** 3
+    if dtype != "f16":
+        for i, e in enumerate((38, 43, 60, -28, -33, -45, -52, -58, -75)):
+            scale[10 + i] = 2.0 ** e
     x = (x.double() * scale).to(dt)
     x[5, 3], x[6, hidden - 1] = float("inf"), float("nan")
     x[7] = torch.finfo(dt).smallest_normal / 4
-    for eps in (1e-6, 0.0):
+    for eps in (1e-6, 0.0, 1e-30, 1e-14):
         dx, dw = rn.rms_norm_backward(dy, x, w, eps)
         check(dy, x, w, 0.0, eps, dx, None)
         ref = R.norm_bwd(dy.double(), dy.double().abs(), x, w, 0.0, eps, 0)
         assert torch.equal(dw.isnan(), ref[2].isnan())
     # without the rows that are not numbers, every column's sum
-    keep = torch.tensor([0, 1, 2, 4, 7, 8, 9, 10, 11], device="cuda")
+    keep = torch.tensor([0, 1, 2, 4] + list(range(7, 20)), device="cuda")
     dy, x = dy[keep].contiguous(), x[keep].contiguous()
     check(dy, x, w, 0.0, 0.0, *rn.rms_norm_backward(dy, x, w, 0.0))
+
+
+def test_first_call_of_a_shape_inside_a_capture():
+    """What a body looks up at its first launch is looked up in a capture, too."""
+    dy, x, w, _ = make("f16", 40, 6136, 12)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, dw = rn.rms_norm_backward(dy, x, w, 1e-6)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(dy, x, w, 0.0, 1e-6, dx, dw)
+
+
+def test_refusals_of_the_workspace():
+    dy, x, w, _ = make("bf16", 8, 4096, 13)
+    dx, dw = torch.empty_like(x), torch.empty(4096, device="cuda")
+    need = rn.rmsnorm_bwd_workspace(8, 4096, rn.BF16, rn.rmsnorm_device_limits()[0])
+    ws = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+
+    def status(ws_at, n, dw_at=dw.data_ptr()):
+        try:
+            rn.rmsnorm_bwd(dy.data_ptr(), x.data_ptr(), w.data_ptr(), dx.data_ptr(), dw_at, ws_at, n,
+                           8, 4096, 0.0, 1e-6, rn.BF16, s)
+        except rn.RmsnormError as e:
+            return e.status
+        return rn.OK
+
+    p = ws.data_ptr()
+    assert status(p, need) == rn.OK and status(p + 16, need) == rn.OK
+    assert status(p, need - 1) == rn.ERR_INVALID_ARG and status(0, need) == rn.ERR_INVALID_ARG
+    assert status(p + 8, need) == rn.ERR_MISALIGNED
+    assert status(dx.data_ptr(), need) == rn.ERR_ALIASING
+    assert status(p, need, p + 64) == rn.ERR_ALIASING
+    assert status(p, need, w.data_ptr()) == rn.ERR_ALIASING
 
 
 def test_no_rows():

@@ -131,23 +131,27 @@ def test_no_rotation_is_the_qk_norm():
 
 # ------------------------------------------------------------------ extreme values
 
-@pytest.mark.parametrize("D,layout", [(128, "plain"), (72, "plain")])
+@pytest.mark.parametrize("D", [128, 72, 20, 9, 1024])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-def test_extreme_heads(dtype, D, layout):
-    """Heads of magnitude 2^+-100, zeros, subnormals, with infinities and NaN;
-    eps 0 and not.  The other heads are not touched by them."""
-    c, g = make(dtype, 24, 4, 2, D, D, layout, 6)
+def test_extreme_heads(dtype, D):
+    """Heads of magnitudes from 2^-110 to 2^103, zeros, subnormals, with
+    infinities and NaN; eps 0, tiny and usual.  The other heads are not touched by
+    them."""
+    c, g = make(dtype, 24, 4, 2, D, D // 2 * 2, "plain", 6)
     dt = R.DT[dtype]
     big, small = ((2.0 ** 100, 2.0 ** -110) if dtype != "f16" else (2.0 ** 11, 2.0 ** -14))
     scale = torch.ones(24, 4, 1, dtype=torch.float64, device="cuda")
     scale[1], scale[2], scale[3, 1], scale[4] = big, small, 0.0, big * 2.0 ** 3
+    if dtype != "f16":
+        for i, e in enumerate((38, 43, 60, -28, -33, -45, -52, -58, -75)):
+            scale[10 + i] = 2.0 ** e
     c["q"] = (c["q"].double() * scale).to(dt)
     c["q"][5, 0, 3] = float("inf")
     c["q"][6, 1, D - 1] = float("nan")
     c["q"][7, 2, 0] = float("-inf")
     c["q"][8, :, :] = torch.finfo(dt).smallest_normal / 4
     dy_q, dy_k = R.rand(g, (24, 4, D), dt), R.rand(g, (24, 2, D), dt)
-    for eps in (1e-6, 0.0):
+    for eps in (1e-6, 0.0, 1e-30, 1e-14):
         qo, ko = rn.qk_norm_rope(c["q"], c["k"], c["qw"], c["kw"], c["cs"], c["pos"], eps,
                                  q_out=torch.empty_like(c["q"]), k_out=torch.empty_like(c["k"]))
         ref, mag = R.heads(c["q"], c["qw"], 0.0, eps, c["rows"], False)
@@ -179,8 +183,8 @@ def test_eps_zero_with_idle_lanes():
 # ------------------------------------------------------------------ positions outside the table
 
 def test_positions_outside_the_table():
-    for D in (128, 72):
-        c, g = make("bf16", 40, 4, 2, D, D, "plain", 7, context=100)
+    for D in (128, 72, 7, 600):
+        c, g = make("bf16", 40, 4, 2, D, D // 2 * 2, "plain", 7, context=100)
         bad = [0, 3, 17, 39]
         c["pos"][bad] = torch.tensor([-1, 100, 1 << 40, -(1 << 62)], device="cuda")
         fill = R.rand(g, (40, 4, D), torch.bfloat16)
@@ -430,9 +434,72 @@ def test_append_saturates_and_keeps_nan():
     assert kc.view(torch.float8_e4m3fn).float().abs().max() == 448.0
 
 
+def test_append_to_caches_at_odd_bytes():
+    """8-bit caches of which no vector of codes is aligned, and 16-bit ones an
+    element off."""
+    c, g = make("bf16", 12, 4, 2, 64, 64, "plain", 27)
+    slots = torch.randperm(32, generator=g, device="cuda")[:12]
+    flat = [torch.zeros(2 * 16 * 2 * 64 + 1, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    kc, vc = (f[1:].view(2, 16, 2, 64) for f in flat)
+    rn.qk_norm_rope_append(c["q"], c["k"], c["v"], c["qw"], c["kw"], c["cs"], c["pos"], slots, kc,
+                           vc, 1e-6, k_scale=0.02, v_scale=0.02)
+    kd, vd = (torch.zeros(2, 16, 2, 64, dtype=torch.uint8, device="cuda") for _ in "kv")
+    rn.qk_norm_rope_append(None, c["k"], c["v"], None, c["kw"], c["cs"], c["pos"], slots, kd, vd,
+                           1e-6, k_scale=0.02, v_scale=0.02)
+    ref, mag = R.heads(c["k"], c["kw"], 0.0, 1e-6, c["rows"], False)
+    sc = torch.tensor(0.02).double().item()
+    for t in (kc, kd):
+        codes = t.contiguous().view(32, -1)[slots].view(torch.float8_e4m3fn).view(12, 2, 64)
+        R.assert_close(codes, (ref / sc).clamp(-448, 448), mag / sc, K_FWD + 3)
+    assert torch.equal(vc.contiguous(), vd)
+    flat = [torch.zeros(2 * 16 * 2 * 64 + 1, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    kc, vc = (f[1:].view(2, 16, 2, 64) for f in flat)
+    rn.qk_norm_rope_append(None, c["k"], c["v"], None, c["kw"], c["cs"], c["pos"], slots, kc, vc,
+                           1e-6)
+    R.assert_close(kc.contiguous().view(32, 2, 64)[slots], ref, mag, K_FWD)
+    assert torch.equal(vc.contiguous().view(32, 2, 64)[slots], c["v"])
+
+
+def test_keys_alone_through_the_c_names():
+    """No q heads: NULL for q everywhere."""
+    c, g = make("bf16", 9, 1, 3, 128, 128, "plain", 28)
+    rope = rn.Rope(c["cs"].data_ptr(), c["pos"].data_ptr(), 4096, 128, 0)
+    s = torch.cuda.current_stream().cuda_stream
+    of = lambda t: rn.Heads(t.data_ptr(), 0, 0)
+    ko, dk = torch.empty_like(c["k"]), torch.empty_like(c["k"])
+    dy = R.rand(g, c["k"].shape, torch.bfloat16)
+    rn.rmsnorm_qk_norm_rope(None, of(c["k"]), None, of(ko), 0, c["kw"].data_ptr(), rope, 9, 0, 3,
+                            128, 0.0, 1e-6, rn.BF16, s)
+    need = rn.rmsnorm_qk_norm_rope_bwd_workspace(128, rn.rmsnorm_device_limits()[0])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    grads = torch.full((2, 128), 7.0, device="cuda")
+    args = (None, of(dy), None, of(c["k"]), None, of(dk), 0, c["kw"].data_ptr(),
+            grads[0].data_ptr(), grads[1].data_ptr(), rope, ws.data_ptr())
+    rn.rmsnorm_qk_norm_rope_bwd(*args, need, 9, 0, 3, 128, 0.0, 1e-6, rn.BF16, s)
+    ref, mag = R.heads(c["k"], c["kw"], 0.0, 1e-6, c["rows"], False)
+    R.assert_close(ko, ref, mag, K_FWD)
+    b = R.heads_bwd(dy, c["k"], c["kw"], 0.0, 1e-6, c["rows"], False)
+    R.assert_close(dk, b[0], b[1], K_DX)
+    R.assert_close(grads[1], b[2], b[3], 129)
+    assert not grads[0].any()
+    # a workspace too small, or not aligned, and outputs inside it
+    for bad, status in (((need - 1,), rn.ERR_INVALID_ARG),):
+        with pytest.raises(rn.RmsnormError) as e:
+            rn.rmsnorm_qk_norm_rope_bwd(*args, *bad, 9, 0, 3, 128, 0.0, 1e-6, rn.BF16, s)
+        assert e.value.status == status
+    with pytest.raises(rn.RmsnormError) as e:
+        rn.rmsnorm_qk_norm_rope_bwd(*args[:-1], ws.data_ptr() + 4, need, 9, 0, 3, 128, 0.0, 1e-6,
+                                    rn.BF16, s)
+    assert e.value.status == rn.ERR_MISALIGNED
+    with pytest.raises(rn.RmsnormError) as e:
+        rn.rmsnorm_qk_norm_rope_bwd(*args[:8], ws.data_ptr() + 512, grads[1].data_ptr(), *args[10:],
+                                    need, 9, 0, 3, 128, 0.0, 1e-6, rn.BF16, s)
+    assert e.value.status == rn.ERR_ALIASING
+
+
 def test_append_slots_outside_the_cache():
-    for D in (128, 72):
-        c, g = make("bf16", 30, 4, 2, D, D, "plain", 25, context=64)
+    for D in (128, 72, 7):
+        c, g = make("bf16", 30, 4, 2, D, D // 2 * 2, "plain", 25, context=64)
         kc, vc = make_cache(g, "bf16", "same", 3, 16, 2, D, "slots")
         k0, v0 = kc.clone(), vc.clone()
         slots = torch.arange(30, device="cuda") + 9
