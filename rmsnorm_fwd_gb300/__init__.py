@@ -14,6 +14,7 @@ tensors, reads their data pointers and the current stream, and calls
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 import threading
 
@@ -659,31 +660,42 @@ _ROPE = struct.Struct("@PPqii")         # rmsnorm_rope_t
 _CACHE = struct.Struct("@PPqqqqqiff0q")  # rmsnorm_paged_cache_t, padded to its end
 
 
-def _launch_on(device, stream, call):
-    """call(raw stream) with `device` current, on `stream` or the device's
-    current stream.  Tensors made in `call` belong to that stream."""
+def _here(device, stream) -> bool:
+    """Whether a call on `device` and `stream` (None: the current one) runs as
+    things stand; else the caller calls itself again inside _there().  Short
+    calls pay for every microsecond on the host."""
     import torch
     if device.index not in _created:
         ensure_context(device.index)
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    raw = torch._C._cuda_getCurrentRawStream
-    if torch.cuda.current_device() == device.index:
-        return call(raw(device.index))
-    with torch.cuda.device(device):
-        return call(raw(device.index))
+    return stream is None and torch.cuda.current_device() == device.index
 
 
-_sms: dict[int, int] = {}
+def _there(device, stream):
+    """The context in which `stream` (and its device), or `device`, is current.
+    Tensors made in it belong to that stream."""
+    import torch
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
+def _stream(device) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=None)
 def _sm_count(index: int) -> int:
     """SM count of the current device, `index` (one that has a context)."""
-    n = _sms.get(index)
-    if n is None:
-        n = _sms[index] = rmsnorm_device_limits()[0]
-    return n
+    return rmsnorm_device_limits()[0]
+
+
+@functools.lru_cache(maxsize=256)
+def _heads_workspace(head_dim: int, sms: int) -> int:
+    return rmsnorm_qk_norm_rope_bwd_workspace(head_dim, sms)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rows_workspace(rows: int, hidden: int, code: int, sms: int) -> int:
+    return rmsnorm_bwd_workspace(rows, hidden, code, sms)
 
 
 def _heads(t, name: str, like=None) -> tuple[bytes, int]:
@@ -775,14 +787,19 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
     A position outside the table leaves its token out and is reported by
     rmsnorm_get_device_status (ERR_BAD_INDEX).  Runs on ``stream`` (default:
     PyTorch's current stream)."""
+    device = q.device
     qh, tokens = _heads(q, "q")
-    head_dim = q.shape[-1]
+    q_heads, head_dim = q.shape[-2:]
     kh, k_heads = None, 0
     if k is not None:
         kh, k_tokens = _heads(k, "k", q)
-        k_heads = k.shape[-2]
-        if k_tokens != tokens or k.shape[-1] != head_dim:
+        k_heads, k_dim = k.shape[-2:]
+        if k_tokens != tokens or k_dim != head_dim:
             raise ValueError("q and k must hold the same number of tokens and one head_dim")
+    if not _here(device, stream):
+        with _there(device, stream):
+            return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, weight_bias,
+                                interleaved, q_out, k_out)
     qo = ko = None
     if q_out is not None:
         _same_shape(q_out, q, "q_out")
@@ -792,13 +809,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
             raise ValueError("k_out without k")
         _same_shape(k_out, k, "k_out")
         ko = _heads(k_out, "k_out", q)[0]
-    rope = _rope(cos_sin, positions, tokens, interleaved, q.device)
-    qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
-    code = torch_dtype_code(q.dtype)
-    fn = _load().rmsnorm_qk_norm_rope
-    _check(_launch_on(q.device, stream, lambda s: fn(
-        qh, kh, qo, ko, qw, kw, rope, tokens, q.shape[-2], k_heads, head_dim, weight_bias, eps,
-        code, s)), "rmsnorm_qk_norm_rope")
+    _check(_load().rmsnorm_qk_norm_rope(
+        qh, kh, qo, ko, _head_weight(q_weight, "q_weight", q),
+        _head_weight(k_weight, "k_weight", q),
+        _rope(cos_sin, positions, tokens, interleaved, device), tokens, q_heads, k_heads,
+        head_dim, weight_bias, eps, torch_dtype_code(q.dtype), _stream(device)),
+        "rmsnorm_qk_norm_rope")
     return q if q_out is None else q_out, k if k_out is None else k_out
 
 
@@ -813,49 +829,53 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     float32 [head_dim] (None with ``weight_grads=False``).  k and dk_out may
     be None.  Other arguments as for ``qk_norm_rope``."""
     import torch
+    device, dtype = q.device, q.dtype
     qh, tokens = _heads(q, "q")
-    head_dim = q.shape[-1]
+    q_shape = q.shape
+    q_heads, head_dim = q_shape[-2:]
+    if not _here(device, stream):
+        with _there(device, stream):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin,
+                                         positions, eps, weight_bias, interleaved, dq, dk,
+                                         weight_grads)
     _same_shape(dq_out, q, "dq_out")
     qy = _heads(dq_out, "dq_out", q)[0]
-    if dq is not None:
-        _same_shape(dq, q, "dq")
-    kh = ky = None
+    kh = ky = kd = None
     k_heads = 0
     if k is not None:
         kh, k_tokens = _heads(k, "k", q)
-        k_heads = k.shape[-2]
-        if k_tokens != tokens or k.shape[-1] != head_dim:
+        k_heads, k_dim = k.shape[-2:]
+        if k_tokens != tokens or k_dim != head_dim:
             raise ValueError("q and k must hold the same number of tokens and one head_dim")
         _same_shape(dk_out, k, "dk_out")
         ky = _heads(dk_out, "dk_out", q)[0]
-        if dk is not None:
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=dtype, device=device)
+            kd = _HEADS.pack(dk.data_ptr(), 0, 0)
+        else:
             _same_shape(dk, k, "dk")
-    rope = _rope(cos_sin, positions, tokens, interleaved, q.device)
-    qw, kw = _head_weight(q_weight, "q_weight", q), _head_weight(k_weight, "k_weight", q)
-    code = torch_dtype_code(q.dtype)
-    fn = _load().rmsnorm_qk_norm_rope_bwd
-    device = q.device
-
-    def call(s):
-        q_grad = torch.empty(q.shape, dtype=q.dtype, device=device) if dq is None else dq
-        qd, kd, k_grad = _heads(q_grad, "dq", q)[0], None, dk
-        if k is not None:
-            if k_grad is None:
-                k_grad = torch.empty(k.shape, dtype=q.dtype, device=device)
-            kd = _heads(k_grad, "dk", q)[0]
-        wp = qp = kp = qg = kg = None
-        need = 0
-        if weight_grads:
-            need = rmsnorm_qk_norm_rope_bwd_workspace(head_dim, _sm_count(device.index))
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-            qg = torch.empty(head_dim, dtype=torch.float32, device=device)
-            kg = torch.empty(head_dim, dtype=torch.float32, device=device)
-            wp, qp, kp = ws.data_ptr(), qg.data_ptr(), kg.data_ptr()
-        _check(fn(qy, ky, qh, kh, qd, kd, qw, kw, qp, kp, rope, wp, need, tokens, q.shape[-2],
-                  k_heads, head_dim, weight_bias, eps, code, s), "rmsnorm_qk_norm_rope_bwd")
-        return q_grad, k_grad, qg, kg
-
-    return _launch_on(device, stream, call)
+            kd = _heads(dk, "dk", q)[0]
+    if dq is None:
+        dq = torch.empty(q_shape, dtype=dtype, device=device)
+        qd = _HEADS.pack(dq.data_ptr(), 0, 0)
+    else:
+        _same_shape(dq, q, "dq")
+        qd = _heads(dq, "dq", q)[0]
+    wp = qp = kp = qg = kg = None
+    need = 0
+    if weight_grads:
+        need = _heads_workspace(head_dim, _sm_count(device.index))
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        qg = torch.empty(head_dim, dtype=torch.float32, device=device)
+        kg = torch.empty(head_dim, dtype=torch.float32, device=device)
+        wp, qp, kp = ws.data_ptr(), qg.data_ptr(), kg.data_ptr()
+    _check(_load().rmsnorm_qk_norm_rope_bwd(
+        qy, ky, qh, kh, qd, kd, _head_weight(q_weight, "q_weight", q),
+        _head_weight(k_weight, "k_weight", q), qp, kp,
+        _rope(cos_sin, positions, tokens, interleaved, device), wp, need, tokens, q_heads,
+        k_heads, head_dim, weight_bias, eps, torch_dtype_code(dtype), _stream(device)),
+        "rmsnorm_qk_norm_rope_bwd")
+    return dq, dk, qg, kg
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, k_cache, v_cache,
@@ -890,6 +910,11 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
         _same_shape(q_out, q, "q_out")
         qo = _heads(q_out, "q_out", k)[0]
     device = k.device
+    if not _here(device, stream):
+        with _there(device, stream):
+            return qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots,
+                                       k_cache, v_cache, eps, weight_bias, interleaved, k_scale,
+                                       v_scale, q_out)
     if slots.dtype != torch.int64:
         raise TypeError("slots must be int64")
     if slots.device != device or slots.numel() != tokens or not slots.is_contiguous():
@@ -909,13 +934,12 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
         raise TypeError("the caches must hold the dtype of k, float8_e4m3fn or uint8")
     cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], st[0], st[1],
                         st[2], e4m3, k_scale, v_scale)
-    rope = _rope(cos_sin, positions, tokens, interleaved, device)
-    qw, kw = _head_weight(q_weight, "q_weight", k), _head_weight(k_weight, "k_weight", k)
-    code = torch_dtype_code(k.dtype)
-    fn = _load().rmsnorm_qk_norm_rope_append
-    _check(_launch_on(device, stream, lambda s: fn(
-        qh, kh, vh, qo, qw, kw, rope, cache, slots.data_ptr(), tokens, q_heads, k_heads, head_dim,
-        weight_bias, eps, code, s)), "rmsnorm_qk_norm_rope_append")
+    _check(_load().rmsnorm_qk_norm_rope_append(
+        qh, kh, vh, qo, _head_weight(q_weight, "q_weight", k),
+        _head_weight(k_weight, "k_weight", k),
+        _rope(cos_sin, positions, tokens, interleaved, device), cache, slots.data_ptr(), tokens,
+        q_heads, k_heads, head_dim, weight_bias, eps, torch_dtype_code(k.dtype),
+        _stream(device)), "rmsnorm_qk_norm_rope_append")
     return q if q_out is None else q_out
 
 
@@ -928,26 +952,26 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
     ``weight_grad=False``)."""
     import torch
     _check_rows(x, weight)
-    device = x.device
+    device, shape, dtype = x.device, x.shape, x.dtype
     for t, name in ((dy, "dy"), (dx, "dx")):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or
-                              t.device != device or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or
+                              not t.is_contiguous()):
             raise ValueError(f"{name} must match x (shape, dtype, device, contiguous)")
     if weight.device != device:
         raise ValueError("weight must be on the device of x")
-    hidden = x.shape[-1]
+    if not _here(device, stream):
+        with _there(device, stream):
+            return rms_norm_backward(dy, x, weight, eps, weight_bias, dx, weight_grad)
+    hidden = shape[-1]
     rows = x.numel() // hidden if hidden else 0
-    code = torch_dtype_code(x.dtype)
-    fn = _load().rmsnorm_bwd
-
-    def call(s):
-        grad = torch.empty_like(x) if dx is None else dx
-        need = rmsnorm_bwd_workspace(rows, hidden, code, _sm_count(device.index))
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        w_grad = torch.empty(hidden, dtype=torch.float32, device=device) if weight_grad else None
-        _check(fn(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), grad.data_ptr(),
-                  w_grad.data_ptr() if weight_grad else None, ws.data_ptr(), need, rows, hidden,
-                  weight_bias, eps, code, s), "rmsnorm_bwd")
-        return grad, w_grad
-
-    return _launch_on(device, stream, call)
+    code = torch_dtype_code(dtype)
+    if dx is None:
+        dx = torch.empty_like(x)
+    need = _rows_workspace(rows, hidden, code, _sm_count(device.index))
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    w_grad = torch.empty(hidden, dtype=torch.float32, device=device) if weight_grad else None
+    _check(_load().rmsnorm_bwd(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), dx.data_ptr(),
+                               w_grad.data_ptr() if weight_grad else None, ws.data_ptr(), need,
+                               rows, hidden, weight_bias, eps, code, _stream(device)),
+           "rmsnorm_bwd")
+    return dx, w_grad
