@@ -46,16 +46,18 @@ struct Parts {
 // Memory bounds it once the warps on an SM have enough bytes on the way and
 // few enough instructions between load and store.  Measured (16384 tokens of
 // 32 + 8 bf16 heads of 128, 338 MB, floor 50.6 us at the copy bandwidth): the
-// scalar body 326.8 us; this one 52.9 us (6.38 TB/s, 95 %).  On the way: one
+// scalar body 326.8 us; this one 52.5 us (6.44 TB/s, 96 %).  On the way: one
 // head a lane with its angles in registers 90 us (80 registers, half the
 // warps); a warp within one tensor instead of choosing q or k lane by lane
 // 84 -> 58 us; the pairing as a template 58 -> 55 us; four heads a lane instead of
 // two 55 -> 53 us.  Slots that hold a warp's vectors in whole lines (slot_vectors)
 // took 5003 tokens of 16 + 8 f16 heads of 256, 64 rotated as neighbours, from
 // 28.0 to 22.7 us (floor 18.5).  Register caps: 64 for four heads (80: 3 %
-// slower), 48 for two (64: 2 % slower, 40: 19 % slower).
+// slower), 48 for two (64: 2 % slower, 40: 19 % slower).  Blocks of four warps (of
+// eight, whose places wait for the slowest: 53.3 us; appending 67.0 for 65.1).
+constexpr int kFwdWarps = 4; // of a block
 template <int DT, int VB, int TPR, int NP, int U, bool APPEND, int MODE>
-__global__ void __launch_bounds__(256, NP == 4 ? 1 : NP == 2 ? 2 : U == 2 ? 5 : 4)
+__global__ void __launch_bounds__(kFwdWarps * 32, NP == 4 ? 2 : NP == 2 ? 4 : U == 2 ? 10 : 8)
 rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
 {
     using E = Elem<DT>;
@@ -65,7 +67,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     pdl_begin();
     const int t = threadIdx.x % TPR;
     const int g = (threadIdx.x & 31) / TPR;
-    const uint32_t item = __shfl_sync(0xFFFFFFFFu, blockIdx.x * 8 + (threadIdx.x >> 5), 0);
+    const uint32_t item = __shfl_sync(0xFFFFFFFFu, blockIdx.x * kFwdWarps + (threadIdx.x >> 5), 0);
     const uint32_t tok32 = item / parts.all;
     uint32_t part = item - tok32 * parts.all;
     const int64_t tok = tok32;
@@ -297,9 +299,9 @@ cudaError_t launch_vec(const RopeArgs &a)
     constexpr int per = U * (32 / TPR); // heads a warp takes
     const uint32_t q = (a.q_heads + per - 1) / per, k = (a.k_heads + per - 1) / per;
     const Parts parts = {q, k, q + k * (APPEND ? 2 : 1)};
-    const int64_t blocks = (a.tokens * parts.all + 7) / 8;
+    const int64_t blocks = (a.tokens * parts.all + kFwdWarps - 1) / kFwdWarps;
     return launch_kernel(rope_kernel<DT, VB, TPR, NP, U, APPEND, MODE>, static_cast<int>(blocks),
-                         256, 0, a.base, a, parts);
+                         kFwdWarps * 32, 0, a.base, a, parts);
 }
 
 // Heads a lane takes.  One, while that leaves fewer than 20 warps an SM: short
