@@ -19,7 +19,6 @@ extern "C" {
  * or a slot outside the cache, found on the device (device status word). */
 enum { RMSNORM_ERR_BAD_INDEX = 11 };
 
-
 /* The heads of one tensor: head h of token t is the head_dim contiguous
  * elements from element t * token_stride + h * head_stride of `data` (a
  * DEVICE pointer).  A stride of 0 stands for the contiguous layout [tokens,
@@ -69,6 +68,7 @@ typedef struct {
  * two vectors' elements) take a vector kernel, others a scalar one.
  * Enqueues one kernel on `stream`; does not synchronise.  Returns RMSNORM_OK,
  * RMSNORM_ERR_INVALID_ARG, RMSNORM_ERR_UNSUPPORTED_DTYPE,
+ * RMSNORM_ERR_MISALIGNED (a pointer that is not on an element's boundary),
  * RMSNORM_ERR_ALIASING, RMSNORM_ERR_NOT_INITIALIZED or RMSNORM_ERR_CUDA. */
 int rmsnorm_qk_norm_rope(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k,
                          const rmsnorm_heads_t *q_out, const rmsnorm_heads_t *k_out,
@@ -94,7 +94,7 @@ int rmsnorm_qk_norm_rope(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k,
  *                   run at the same time need a workspace each.
  * A tensor with no heads gets a zero weight gradient.  Enqueues one kernel,
  * and a second small one for the weights' gradients.  Otherwise as
- * rmsnorm_qk_norm_rope; RMSNORM_ERR_MISALIGNED for the workspace. */
+ * rmsnorm_qk_norm_rope; RMSNORM_ERR_MISALIGNED for the workspace, too. */
 int rmsnorm_qk_norm_rope_bwd(const rmsnorm_heads_t *dq_out, const rmsnorm_heads_t *dk_out,
                              const rmsnorm_heads_t *q, const rmsnorm_heads_t *k,
                              const rmsnorm_heads_t *dq, const rmsnorm_heads_t *dk,
@@ -122,8 +122,9 @@ typedef struct {
     int64_t slot_stride;
     int64_t head_stride;
     int32_t e4m3;  /* 0: elements of the call's dtype; 1: E4M3 bytes */
-    float k_scale; /* E4M3: a value is stored as E4M3(value / scale), nearest-even, */
-    float v_scale; /* saturating at +-448 (NaN stays NaN); positive and finite */
+    float k_scale; /* E4M3: a value is stored as E4M3(value * (1 / scale)), 1 / scale in fp32, */
+    float v_scale; /* nearest-even, saturating at +-448 (NaN stays NaN); scale and its
+                    * reciprocal positive and finite */
 } rmsnorm_paged_cache_t;
 
 /* rmsnorm_qk_norm_rope with the keys and values appended to a paged cache in

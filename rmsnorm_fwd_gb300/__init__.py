@@ -674,7 +674,11 @@ def _there(device, stream):
     """The context in which `stream` (and its device), or `device`, is current.
     Tensors made in it belong to that stream."""
     import torch
-    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream must be on the device of the tensors")
+    return torch.cuda.stream(stream)
 
 
 def _stream(device) -> int:
@@ -825,7 +829,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     dq_weight, dk_weight) from the gradients of its outputs and its inputs q
     and k as they were before the call (so that call must not be in place).
     dq / dk: optional outputs, which may be dq_out / dk_out or q / k
-    themselves; by default new contiguous tensors.  The weights' gradients are
+    themselves; by default new contiguous tensors.  Expanded gradients (stride
+    0) are refused: make them contiguous.  The weights' gradients are
     float32 [head_dim] (None with ``weight_grads=False``).  k and dk_out may
     be None.  Other arguments as for ``qk_norm_rope``."""
     import torch

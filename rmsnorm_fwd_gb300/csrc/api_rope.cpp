@@ -262,6 +262,8 @@ int rmsnorm_qk_norm_rope(const rmsnorm_heads_t *q, const rmsnorm_heads_t *k,
     for (const Heads *h : {&qi, &ki, &qo, &ko})
         if (h->p % es != 0)
             return RMSNORM_ERR_MISALIGNED;
+    if (addr(q_weight) % es != 0 || addr(k_weight) % es != 0)
+        return RMSNORM_ERR_MISALIGNED;
     if (bad_alias(qo, qi) || bad_alias(ko, ki) || heads_overlap(qo, ko) || heads_overlap(qo, ki) ||
         heads_overlap(ko, qi) || hits_inputs(qo, *rope, q_weight, k_weight) ||
         hits_inputs(ko, *rope, q_weight, k_weight))
@@ -329,6 +331,8 @@ int rmsnorm_qk_norm_rope_append(const rmsnorm_heads_t *q, const rmsnorm_heads_t 
     for (const Heads *h : {&qi, &ki, &vi, &qo})
         if (h->p % es != 0)
             return RMSNORM_ERR_MISALIGNED;
+    if (addr(q_weight) % es != 0 || addr(k_weight) % es != 0)
+        return RMSNORM_ERR_MISALIGNED;
     if (addr(cache->k) % ces != 0 || addr(cache->v) % ces != 0 || addr(slots) % 8 != 0)
         return RMSNORM_ERR_MISALIGNED;
     if (bad_alias(qo, qi) || heads_overlap(qo, ki) || heads_overlap(qo, vi) ||
@@ -434,6 +438,8 @@ int rmsnorm_qk_norm_rope_bwd(const rmsnorm_heads_t *dq_out, const rmsnorm_heads_
     for (const Heads *h : {&qy, &ky, &qi, &ki, &qd, &kd})
         if (h->p % es != 0)
             return RMSNORM_ERR_MISALIGNED;
+    if (addr(q_weight) % es != 0 || addr(k_weight) % es != 0)
+        return RMSNORM_ERR_MISALIGNED;
     if (bad_alias(qd, qy) || bad_alias(qd, qi) || bad_alias(kd, ky) || bad_alias(kd, ki) ||
         heads_overlap(qd, kd) || heads_overlap(qd, ky) || heads_overlap(qd, ki) ||
         heads_overlap(kd, qy) || heads_overlap(kd, qi) ||

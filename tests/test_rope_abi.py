@@ -53,6 +53,8 @@ SIZES = [
     (dict(rp=rope(positions=ptr(21) + 4)), rn.ERR_MISALIGNED),
     (dict(rp=rope(cos_sin=ptr(20) + 2)), rn.ERR_MISALIGNED),
     (dict(q=H(ptr(0) + 1)), rn.ERR_MISALIGNED),
+    (dict(qw=ptr(10) + 1), rn.ERR_MISALIGNED), (dict(kw=ptr(11) + 1), rn.ERR_MISALIGNED),
+    (dict(kw=ptr(11) + 2, dtype=rn.F32), rn.ERR_MISALIGNED),
     (dict(q=None), rn.ERR_INVALID_ARG), (dict(k=H(0)), rn.ERR_INVALID_ARG),
     (dict(qw=None), rn.ERR_INVALID_ARG), (dict(kw=None), rn.ERR_INVALID_ARG),
     (dict(q=H(ptr(0), -1)), rn.ERR_INVALID_ARG),
@@ -275,6 +277,14 @@ class Fake:
 
     def data_ptr(self):
         return P
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = "cuda:1"
+
+    with pytest.raises(ValueError):
+        rn._there("cuda:0", Stream())
 
 
 def test_packed_structures_are_the_structures():
