@@ -670,14 +670,17 @@ def _here(device, stream) -> bool:
     return stream is None and torch.cuda.current_device() == device.index
 
 
-def _there(device, stream):
+def _there(device, stream, *tensors):
     """The context in which `stream` (and its device), or `device`, is current.
-    Tensors made in it belong to that stream."""
+    Tensors made in it belong to that stream; `tensors` are used on it."""
     import torch
     if stream is None:
         return torch.cuda.device(device)
     if stream.device != device:
         raise ValueError("stream must be on the device of the tensors")
+    for t in tensors:  # their memory is not given out again before `stream` is done with it
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -705,7 +708,7 @@ def _rows_workspace(rows: int, hidden: int, code: int, sms: int) -> int:
 def _heads(t, name: str, like=None) -> tuple[bytes, int]:
     """(rmsnorm_heads_t, tokens) of a CUDA tensor [..., heads, head_dim] whose
     leading dimensions step evenly over the tokens."""
-    if not t.is_cuda:
+    if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     shape, strides = t.shape, t.stride()
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
@@ -747,6 +750,8 @@ def _rope(cos_sin, positions, tokens: int, interleaved: bool, device) -> bytes:
     import torch
     if cos_sin is None:
         return _NO_ROPE
+    if positions is None:
+        raise ValueError("cos_sin without positions")
     if cos_sin.dtype != torch.float32 or positions.dtype != torch.int64:
         raise TypeError("cos_sin must be float32 and positions int64")
     if cos_sin.device != device or positions.device != device:
@@ -772,8 +777,8 @@ def _head_weight(w, name: str, like):
 
 
 def _same_shape(t, like, name: str) -> None:
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have the shape of its input")
+    if t is None or t.shape != like.shape:
+        raise ValueError(f"{name} must be given, with the shape of its input")
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
@@ -801,7 +806,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
         if k_tokens != tokens or k_dim != head_dim:
             raise ValueError("q and k must hold the same number of tokens and one head_dim")
     if not _here(device, stream):
-        with _there(device, stream):
+        with _there(device, stream, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out):
             return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, weight_bias,
                                 interleaved, q_out, k_out)
     qo = ko = None
@@ -839,7 +844,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     q_shape = q.shape
     q_heads, head_dim = q_shape[-2:]
     if not _here(device, stream):
-        with _there(device, stream):
+        with _there(device, stream, dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions,
+                    dq, dk):
             return qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin,
                                          positions, eps, weight_bias, interleaved, dq, dk,
                                          weight_grads)
@@ -916,11 +922,12 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
         qo = _heads(q_out, "q_out", k)[0]
     device = k.device
     if not _here(device, stream):
-        with _there(device, stream):
+        with _there(device, stream, q, k, v, q_weight, k_weight, cos_sin, positions, slots,
+                    k_cache, v_cache, q_out):
             return qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots,
                                        k_cache, v_cache, eps, weight_bias, interleaved, k_scale,
                                        v_scale, q_out)
-    if slots.dtype != torch.int64:
+    if slots is None or slots.dtype != torch.int64:
         raise TypeError("slots must be int64")
     if slots.device != device or slots.numel() != tokens or not slots.is_contiguous():
         raise ValueError("slots must be contiguous, one for each token, on the device of k")
@@ -958,6 +965,8 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
     import torch
     _check_rows(x, weight)
     device, shape, dtype = x.device, x.shape, x.dtype
+    if dy is None:
+        raise ValueError("dy must be given")
     for t, name in ((dy, "dy"), (dx, "dx")):
         if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or
                               not t.is_contiguous()):
@@ -965,7 +974,7 @@ def rms_norm_backward(dy, x, weight, eps: float, weight_bias: float = -0.0, dx=N
     if weight.device != device:
         raise ValueError("weight must be on the device of x")
     if not _here(device, stream):
-        with _there(device, stream):
+        with _there(device, stream, dy, x, weight, dx):
             return rms_norm_backward(dy, x, weight, eps, weight_bias, dx, weight_grad)
     hidden = shape[-1]
     rows = x.numel() // hidden if hidden else 0

@@ -567,6 +567,115 @@ def test_other_streams_and_two_calls_at_once():
             assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_inputs_freed_right_after_a_call_on_another_stream():
+    """The inputs' memory is not given out again before that stream is done."""
+    c, g = make("bf16", 4000, 16, 4, 128, 128, "plain", 33)
+    want = rn.qk_norm_rope(c["q"], c["k"], c["qw"], c["kw"], c["cs"], c["pos"], 1e-6,
+                           q_out=torch.empty_like(c["q"]), k_out=torch.empty_like(c["k"]))
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        q, k = c["q"].clone(), c["k"].clone()
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2_000_000)  # a millisecond: the call below waits behind it
+        rn.qk_norm_rope(q, k, c["qw"], c["kw"], c["cs"], c["pos"], 1e-6, q_out=qo, k_out=ko,
+                        stream=s)
+        del q, k
+        torch.full_like(c["q"], 7.0)       # would take their place
+        torch.full_like(c["k"], 7.0)
+        s.synchronize()
+        assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+
+def test_without_dependent_launches():
+    """The same bits with programmatic dependent launch off."""
+    c, g = make("bf16", 900, 16, 4, 128, 128, "wide", 34)
+    dy = R.rand(g, (900, 16, 128), torch.bfloat16), R.rand(g, (900, 4, 128), torch.bfloat16)
+    args = (c["q"], c["k"], c["qw"], c["kw"], c["cs"], c["pos"], 1e-6)
+
+    def step():
+        qo, ko = rn.qk_norm_rope(*args, q_out=torch.empty(900, 16, 128, device="cuda",
+                                                          dtype=torch.bfloat16),
+                                 k_out=torch.empty(900, 4, 128, device="cuda",
+                                                   dtype=torch.bfloat16))
+        return qo, ko, *rn.qk_norm_rope_backward(qo, ko, *args)
+
+    was = rn.rmsnorm_get_pdl()
+    try:
+        rn.rmsnorm_set_pdl(True)
+        a = [step() for _ in range(4)][-1]
+        rn.rmsnorm_set_pdl(False)
+        b = step()
+    finally:
+        rn.rmsnorm_set_pdl(was)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_threads_at_once():
+    """Two host threads with their own streams and tensors."""
+    import threading
+    sets = [make("bf16", 700 + 99 * i, 8, 2, 128, 128, "plain", 35 + i) for i in range(2)]
+    want, got = [None, None], [None, None]
+
+    def work(i, out, n):
+        c, _ = sets[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(n):
+                out[i] = rn.qk_norm_rope_backward(c["q"], c["k"], c["q"], c["k"], c["qw"], c["kw"],
+                                                  c["cs"], c["pos"], 1e-6)
+            torch.cuda.current_stream().synchronize()
+
+    for i in range(2):
+        work(i, want, 1)
+    threads = [threading.Thread(target=work, args=(i, got, 50)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_refusals_of_tensors():
+    c, _ = make("bf16", 6, 4, 2, 64, 64, "plain", 37)
+    q, k, v, w, cs, pos = c["q"], c["k"], c["v"], c["qw"], c["cs"], c["pos"]
+    kc = torch.zeros(2, 4, 2, 64, device="cuda", dtype=torch.bfloat16)
+    slots = torch.arange(6, device="cuda")
+    ap = lambda **kw: rn.qk_norm_rope_append(**{**dict(
+        q=q, k=k, v=v, q_weight=w, k_weight=w, cos_sin=cs, positions=pos, slots=slots, k_cache=kc,
+        v_cache=kc.clone(), eps=1e-6, q_out=torch.empty_like(q)), **kw})
+    ap()
+    for kw in (dict(slots=slots[:5]), dict(slots=slots.cpu()), dict(k_cache=kc[..., :32]),
+               dict(v_cache=kc.transpose(0, 1)), dict(positions=pos[:5]), dict(positions=None),
+               dict(cos_sin=cs[:, ::2]), dict(v=v[:, :1]), dict(q=q[:5]), dict(k=k[:, :, :32]),
+               dict(q_out=q[:5]), dict(q=q.expand(6, 4, 64)[:, :1].expand(6, 4, 64)),
+               dict(v_cache=kc.expand(2, 4, 2, 64)[:, :, :1].expand(2, 4, 2, 64)),
+               dict(q=None, q_out=q), dict(k=q[0])):
+        with pytest.raises(ValueError):
+            ap(**kw)
+    for kw in (dict(slots=slots.int()), dict(positions=pos.int()), dict(cos_sin=cs.double()),
+               dict(q_weight=w.float()), dict(v=v.float()), dict(k_cache=kc.float(),
+                                                                 v_cache=kc.float()),
+               dict(slots=None)):
+        with pytest.raises(TypeError):
+            ap(**kw)
+    with pytest.raises(rn.RmsnormError) as e:      # one cache for both
+        ap(v_cache=kc)
+    assert e.value.status == rn.ERR_ALIASING
+    with pytest.raises(ValueError):
+        rn.qk_norm_rope(q, k, w, w, cs, pos, 1e-6, k_out=k[:5])
+    with pytest.raises(ValueError):
+        rn.qk_norm_rope(q, None, w, None, cs, pos, 1e-6, k_out=k)
+    with pytest.raises(rn.RmsnormError) as e:
+        rn.qk_norm_rope(q, k, w, None, cs, pos, 1e-6)
+    assert e.value.status == rn.ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        rn.qk_norm_rope_backward(q, None, q, k, w, w, cs, pos, 1e-6)
+    with pytest.raises(ValueError):
+        rn.qk_norm_rope_backward(q[:1, :1].expand(6, 4, 64), k, q, k, w, w, cs, pos, 1e-6)
+
+
 def test_captured_and_replayed():
     """Forward, gradient and append in one graph; replays follow new inputs,
     positions and slots; a second graph replayed in turn keeps its own results."""

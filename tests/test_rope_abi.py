@@ -178,6 +178,10 @@ def append(q=H(ptr(0)), k=H(ptr(1)), v=H(ptr(2)), qo=None, qw=ptr(10), kw=ptr(11
                                                   slots, T, hq, hk, D, bias, eps, dtype, None)
 
 
+def test_status_of_an_index_found_on_the_device():
+    assert rn.rmsnorm_status_string(rn.ERR_BAD_INDEX) != "unknown status"
+
+
 def test_append_arguments():
     for kw, status in SIZES:
         if not ({"q", "k", "qw", "kw"} & set(kw)):
