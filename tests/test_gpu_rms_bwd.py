@@ -322,3 +322,20 @@ def test_serving_prompt_then_tokens():
     turn = lambda t: R.heads(t, w, 0.0, 1e-6, cs[:T], False)[0]
     want = attention(turn(qkv[:, :hq]), turn(qkv[:, hq:hq + hk]), qkv[:, hq + hk:].double())
     assert (got.double() - want).abs().max() <= R.U * 512 * want.abs().max()
+
+
+def test_the_readme_examples_run():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    blocks = re.findall(r"```python\n(.*?)```", text, re.S)
+    scope = {}
+    for b in blocks:
+        exec(b, scope)
+    torch.cuda.synchronize()
+    ref = R.heads(scope["k"], scope["kw"], 0.0, 1e-6, scope["table"], False)
+    R.assert_close(scope["k_cache"].view(-1, 8, 128)[64:64 + 4096], *ref, 32)
+    b = R.heads_bwd(scope["ko"], scope["k"], scope["kw"], 0.0, 1e-6, scope["table"], False)
+    R.assert_close(scope["dk"], b[0], b[1], 128)
+    R.assert_close(scope["dkw"], b[2], b[3], 128 + 4096 * 8 / 1000)
