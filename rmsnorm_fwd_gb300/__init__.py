@@ -705,14 +705,14 @@ def _rows_workspace(rows: int, hidden: int, code: int, sms: int) -> int:
     return rmsnorm_bwd_workspace(rows, hidden, code, sms)
 
 
-def _heads(t, name: str, like=None) -> tuple[bytes, int]:
+def _heads(t, name: str, dtype, device) -> tuple[bytes, int]:
     """(rmsnorm_heads_t, tokens) of a CUDA tensor [..., heads, head_dim] whose
     leading dimensions step evenly over the tokens."""
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    shape, strides = t.shape, t.stride()
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if t.dtype is not dtype or t.device != device:
         raise TypeError(f"{name} must have the dtype and device of the other tensors")
+    shape, strides = t.shape, t.stride()
     if len(shape) == 3:
         tokens, heads, dim = shape
         step, head_step, last = strides
@@ -731,13 +731,13 @@ def _heads(t, name: str, like=None) -> tuple[bytes, int]:
                 tokens *= n
     else:
         raise ValueError(f"{name} must be [..., tokens, heads, head_dim]")
-    if dim > 1 and last != 1:
+    if last != 1 and dim > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     if heads == 1:
         head_step = 0
-    elif head_step == 0 or (tokens > 1 and step == 0):
+    elif head_step == 0:
         raise ValueError(f"{name} must not be an expanded tensor")
-    if tokens > 1 and step == 0:
+    if step == 0 and tokens > 1:
         raise ValueError(f"{name} must not be an expanded tensor")
     return _HEADS.pack(t.data_ptr(), step, head_step), tokens
 
@@ -766,12 +766,12 @@ def _rope(cos_sin, positions, tokens: int, interleaved: bool, device) -> bytes:
                       1 if interleaved else 0)
 
 
-def _head_weight(w, name: str, like):
+def _head_weight(w, name: str, head_dim: int, dtype, device):
     if w is None:
         return None
-    if w.dtype != like.dtype or w.device != like.device:
+    if w.dtype is not dtype or w.device != device:
         raise TypeError(f"{name} must have the dtype and device of its heads")
-    if w.numel() != like.shape[-1] or not w.is_contiguous():
+    if w.numel() != head_dim or not w.is_contiguous():
         raise ValueError(f"{name} must be contiguous, with head_dim elements")
     return w.data_ptr()
 
@@ -796,12 +796,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
     A position outside the table leaves its token out and is reported by
     rmsnorm_get_device_status (ERR_BAD_INDEX).  Runs on ``stream`` (default:
     PyTorch's current stream)."""
-    device = q.device
-    qh, tokens = _heads(q, "q")
+    if q is None:
+        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
+    device, dtype = q.device, q.dtype
+    qh, tokens = _heads(q, "q", dtype, device)
     q_heads, head_dim = q.shape[-2:]
     kh, k_heads = None, 0
     if k is not None:
-        kh, k_tokens = _heads(k, "k", q)
+        kh, k_tokens = _heads(k, "k", dtype, device)
         k_heads, k_dim = k.shape[-2:]
         if k_tokens != tokens or k_dim != head_dim:
             raise ValueError("q and k must hold the same number of tokens and one head_dim")
@@ -812,17 +814,17 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float,
     qo = ko = None
     if q_out is not None:
         _same_shape(q_out, q, "q_out")
-        qo = _heads(q_out, "q_out", q)[0]
+        qo = _heads(q_out, "q_out", dtype, device)[0]
     if k_out is not None:
         if k is None:
             raise ValueError("k_out without k")
         _same_shape(k_out, k, "k_out")
-        ko = _heads(k_out, "k_out", q)[0]
+        ko = _heads(k_out, "k_out", dtype, device)[0]
     _check(_load().rmsnorm_qk_norm_rope(
-        qh, kh, qo, ko, _head_weight(q_weight, "q_weight", q),
-        _head_weight(k_weight, "k_weight", q),
+        qh, kh, qo, ko, _head_weight(q_weight, "q_weight", head_dim, dtype, device),
+        _head_weight(k_weight, "k_weight", head_dim, dtype, device),
         _rope(cos_sin, positions, tokens, interleaved, device), tokens, q_heads, k_heads,
-        head_dim, weight_bias, eps, torch_dtype_code(q.dtype), _stream(device)),
+        head_dim, weight_bias, eps, torch_dtype_code(dtype), _stream(device)),
         "rmsnorm_qk_norm_rope")
     return q if q_out is None else q_out, k if k_out is None else k_out
 
@@ -839,8 +841,10 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
     float32 [head_dim] (None with ``weight_grads=False``).  k and dk_out may
     be None.  Other arguments as for ``qk_norm_rope``."""
     import torch
+    if q is None:
+        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
     device, dtype = q.device, q.dtype
-    qh, tokens = _heads(q, "q")
+    qh, tokens = _heads(q, "q", dtype, device)
     q_shape = q.shape
     q_heads, head_dim = q_shape[-2:]
     if not _here(device, stream):
@@ -850,28 +854,28 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
                                          positions, eps, weight_bias, interleaved, dq, dk,
                                          weight_grads)
     _same_shape(dq_out, q, "dq_out")
-    qy = _heads(dq_out, "dq_out", q)[0]
+    qy = _heads(dq_out, "dq_out", dtype, device)[0]
     kh = ky = kd = None
     k_heads = 0
     if k is not None:
-        kh, k_tokens = _heads(k, "k", q)
+        kh, k_tokens = _heads(k, "k", dtype, device)
         k_heads, k_dim = k.shape[-2:]
         if k_tokens != tokens or k_dim != head_dim:
             raise ValueError("q and k must hold the same number of tokens and one head_dim")
         _same_shape(dk_out, k, "dk_out")
-        ky = _heads(dk_out, "dk_out", q)[0]
+        ky = _heads(dk_out, "dk_out", dtype, device)[0]
         if dk is None:
             dk = torch.empty(k.shape, dtype=dtype, device=device)
             kd = _HEADS.pack(dk.data_ptr(), 0, 0)
         else:
             _same_shape(dk, k, "dk")
-            kd = _heads(dk, "dk", q)[0]
+            kd = _heads(dk, "dk", dtype, device)[0]
     if dq is None:
         dq = torch.empty(q_shape, dtype=dtype, device=device)
         qd = _HEADS.pack(dq.data_ptr(), 0, 0)
     else:
         _same_shape(dq, q, "dq")
-        qd = _heads(dq, "dq", q)[0]
+        qd = _heads(dq, "dq", dtype, device)[0]
     wp = qp = kp = qg = kg = None
     need = 0
     if weight_grads:
@@ -881,8 +885,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
         kg = torch.empty(head_dim, dtype=torch.float32, device=device)
         wp, qp, kp = ws.data_ptr(), qg.data_ptr(), kg.data_ptr()
     _check(_load().rmsnorm_qk_norm_rope_bwd(
-        qy, ky, qh, kh, qd, kd, _head_weight(q_weight, "q_weight", q),
-        _head_weight(k_weight, "k_weight", q), qp, kp,
+        qy, ky, qh, kh, qd, kd, _head_weight(q_weight, "q_weight", head_dim, dtype, device),
+        _head_weight(k_weight, "k_weight", head_dim, dtype, device), qp, kp,
         _rope(cos_sin, positions, tokens, interleaved, device), wp, need, tokens, q_heads,
         k_heads, head_dim, weight_bias, eps, torch_dtype_code(dtype), _stream(device)),
         "rmsnorm_qk_norm_rope_bwd")
@@ -904,12 +908,15 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
     value / scale (float8_e4m3fn or uint8).  Weights None: the rotation alone.
     k and v are left as they were; ``q`` may be None."""
     import torch
-    kh, tokens = _heads(k, "k")
-    vh, v_tokens = _heads(v, "v", k)
+    if k is None:
+        raise ValueError("k must be a CUDA tensor (there is no CPU path)")
+    device, k_dtype = k.device, k.dtype
+    kh, tokens = _heads(k, "k", k_dtype, device)
+    vh, v_tokens = _heads(v, "v", k_dtype, device)
     k_heads, head_dim = k.shape[-2:]
     qh, q_heads, q_tokens, qo = None, 0, tokens, None
     if q is not None:
-        qh, q_tokens = _heads(q, "q", k)
+        qh, q_tokens = _heads(q, "q", k_dtype, device)
         q_heads = q.shape[-2]
         if q.shape[-1] != head_dim:
             raise ValueError("q and k must hold one head_dim")
@@ -919,8 +926,7 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
         if q is None:
             raise ValueError("q_out without q")
         _same_shape(q_out, q, "q_out")
-        qo = _heads(q_out, "q_out", k)[0]
-    device = k.device
+        qo = _heads(q_out, "q_out", k_dtype, device)[0]
     if not _here(device, stream):
         with _there(device, stream, q, k, v, q_weight, k_weight, cos_sin, positions, slots,
                     k_cache, v_cache, q_out):
@@ -941,16 +947,16 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, 
         raise TypeError("k_cache and v_cache must have one dtype and the device of k")
     if head_dim > 1 and st[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
-    e4m3 = dtype != k.dtype
+    e4m3 = dtype is not k_dtype
     if e4m3 and dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError("the caches must hold the dtype of k, float8_e4m3fn or uint8")
     cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], st[0], st[1],
                         st[2], e4m3, k_scale, v_scale)
     _check(_load().rmsnorm_qk_norm_rope_append(
-        qh, kh, vh, qo, _head_weight(q_weight, "q_weight", k),
-        _head_weight(k_weight, "k_weight", k),
+        qh, kh, vh, qo, _head_weight(q_weight, "q_weight", head_dim, k_dtype, device),
+        _head_weight(k_weight, "k_weight", head_dim, k_dtype, device),
         _rope(cos_sin, positions, tokens, interleaved, device), cache, slots.data_ptr(), tokens,
-        q_heads, k_heads, head_dim, weight_bias, eps, torch_dtype_code(k.dtype),
+        q_heads, k_heads, head_dim, weight_bias, eps, torch_dtype_code(k_dtype),
         _stream(device)), "rmsnorm_qk_norm_rope_append")
     return q if q_out is None else q_out
 

@@ -304,7 +304,7 @@ def test_packed_structures_are_the_structures():
 
 def test_layouts_of_tensors():
     def of(shape, strides):
-        packed, tokens = rn._heads(Fake(shape, strides), "q")
+        packed, tokens = rn._heads(Fake(shape, strides), "q", Fake.dtype, Fake.device)
         return rn.Heads.from_buffer_copy(packed), tokens
 
     h, n = of((5, 8, 64), (512, 64, 1))
