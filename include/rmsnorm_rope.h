@@ -163,10 +163,11 @@ int rmsnorm_qk_norm_rope_append(const rmsnorm_heads_t *q, const rmsnorm_heads_t 
  *              rmsnorm_bwd_workspace gives.  Calls that may run at the same time
  *              need a workspace each.
  * The statistic is formed as in rmsnorm_fwd, over the types' whole range.
- * Enqueues one kernel on `stream`, and a second small one for dweight (rows of
- * more than 16384 elements: up to four); does not synchronise.  Returns the
- * statuses of rmsnorm_fwd; RMSNORM_ERR_INVALID_ARG for a workspace that is too
- * small, RMSNORM_ERR_MISALIGNED for one that is not 16-byte aligned. */
+ * Enqueues one kernel on `stream`, and a second small one for dweight (rows too
+ * long for the registers, of more than 8192 or 16384 elements: up to four); does
+ * not synchronise.  Returns the statuses of rmsnorm_fwd; RMSNORM_ERR_INVALID_ARG
+ * for a workspace that is too small, RMSNORM_ERR_MISALIGNED for one that is not
+ * 16-byte aligned. */
 int rmsnorm_bwd(const void *dy, const void *x, const void *weight, void *dx, float *dweight,
                 void *workspace, size_t workspace_bytes, int64_t rows, int64_t hidden,
                 float weight_bias, float eps, int dtype, void *stream);

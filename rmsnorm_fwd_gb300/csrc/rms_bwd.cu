@@ -15,7 +15,8 @@ namespace {
 
 // ---- rows too long for the registers: statistics, columns, then dx.  Three
 // passes, because such a row does not fit on chip and dx may overwrite dy or
-// x, which the columns' sums still need.
+// x, which the columns' sums still need (two where it does not).  2000 x 30000
+// bf16 (360 MB, floor 53.9 us): 157 us; element by element, as odd rows are, 358.
 
 struct RowStat {
     float r, pre, m;
@@ -33,12 +34,52 @@ __device__ inline float block_sum(float s, float *part)
     return group_allreduce<32>(lane < warps ? part[lane] : 0.f);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(512)
-rms_bwd_stats_kernel(const void *dy, const void *x, const void *w, RowStat *stat, int64_t rows,
-                     int64_t hidden, float bias, float eps)
+// N elements from element j on: a vector, or one by itself.
+template <int DT, int N> __device__ inline void ld_row(float (&f)[N], const char *p, int64_t j)
 {
-    using E = Elem<DT>;
+    if constexpr (N == 1) {
+        f[0] = Elem<DT>::widen1(p, j);
+    } else {
+        Vec<16> v;
+        ld_head(v, p + j * Elem<DT>::kSize);
+        widen_vec<DT, 16>(f, v);
+    }
+}
+template <int DT, int N> __device__ inline void st_row(char *p, int64_t j, const float (&f)[N])
+{
+    if constexpr (N == 1) {
+        Elem<DT>::store1(p, j, f[0]);
+    } else {
+        Vec<16> v;
+        narrow_vec<DT, 16>(v, f);
+        st_head(p + j * Elem<DT>::kSize, v);
+    }
+}
+
+// dx of one row.
+template <int DT, int N>
+__device__ inline void row_dx(const char *dy, const char *x, const char *w, char *dx, int64_t base,
+                              int64_t hidden, float bias, const RowStat &f)
+{
+    for (int64_t j = threadIdx.x * N; j < hidden; j += blockDim.x * N) {
+        float a[N], b[N], g[N];
+        ld_row<DT>(a, x, base + j);
+        ld_row<DT>(b, dy, base + j);
+        ld_row<DT>(g, w, j);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            a[i] = fmaf(b[i], g[i] + bias, -(a[i] * f.pre * f.r * f.m)) * f.r * f.pre;
+        st_row<DT>(dx, base + j, a);
+    }
+}
+
+// A row's statistics and, where dx overwrites neither dy nor x (`with_dx`),
+// dx, while the row is still in L2.
+template <int DT, int N>
+__global__ void __launch_bounds__(512)
+rms_bwd_stats_kernel(const char *dy, const char *x, const char *w, char *dx, RowStat *stat,
+                     int64_t rows, int64_t hidden, float bias, float eps, bool with_dx)
+{
     __shared__ float part[32];
     pdl_begin();
     const float n = static_cast<float>(hidden);
@@ -46,65 +87,75 @@ rms_bwd_stats_kernel(const void *dy, const void *x, const void *w, RowStat *stat
         const int64_t base = row * hidden;
         auto sum = [&](float k) {
             float s = 0.f;
-            for (int64_t j = threadIdx.x; j < hidden; j += blockDim.x) {
-                const float v = E::widen1(x, base + j) * k;
-                s = fmaf(v, v, s);
+            for (int64_t j = threadIdx.x * N; j < hidden; j += blockDim.x * N) {
+                float a[N];
+                ld_row<DT>(a, x, base + j);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    s = fmaf(a[i] * k, a[i] * k, s);
             }
             return block_sum(s, part);
         };
         const RowScale f = row_scale<DT>(sum(1.f), n, eps, sum);
         float m = 0.f;
-        for (int64_t j = threadIdx.x; j < hidden; j += blockDim.x)
-            m = fmaf(E::widen1(dy, base + j) * (E::widen1(w, j) + bias),
-                     E::widen1(x, base + j) * f.pre * f.r, m);
+        for (int64_t j = threadIdx.x * N; j < hidden; j += blockDim.x * N) {
+            float a[N], b[N], g[N];
+            ld_row<DT>(a, x, base + j);
+            ld_row<DT>(b, dy, base + j);
+            ld_row<DT>(g, w, j);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                m = fmaf(b[i] * (g[i] + bias), a[i] * f.pre * f.r, m);
+        }
         m = block_sum(m, part) / n;
+        const RowStat s = {f.r, f.pre, m};
         if (threadIdx.x == 0)
-            stat[row] = {f.r, f.pre, m};
+            stat[row] = s;
+        if (with_dx)
+            row_dx<DT, N>(dy, x, w, dx, base, hidden, bias, s);
     }
 }
 
-// Columns: block (column block, chunk of rows); a thread per column.
-template <int DT>
+// Columns: block (column block, chunk of rows); a thread for N columns.
+template <int DT, int N>
 __global__ void __launch_bounds__(256)
-rms_bwd_columns_kernel(const void *dy, const void *x, const RowStat *stat, float *part,
+rms_bwd_columns_kernel(const char *dy, const char *x, const RowStat *stat, float *part,
                        int64_t rows, int64_t hidden, int64_t col_blocks, int chunks)
 {
-    using E = Elem<DT>;
     pdl_begin();
     const int64_t chunk = blockIdx.x / col_blocks;
-    const int64_t col = (blockIdx.x - chunk * col_blocks) * 256 + threadIdx.x;
+    const int64_t col = ((blockIdx.x - chunk * col_blocks) * 256 + threadIdx.x) * N;
     if (col >= hidden)
         return;
-    float s = 0.f;
+    float s[N] = {};
     for (int64_t row = chunk; row < rows; row += chunks) {
         const RowStat f = stat[row];
-        s = fmaf(E::widen1(dy, row * hidden + col),
-                 E::widen1(x, row * hidden + col) * f.pre * f.r, s);
+        float a[N], b[N];
+        ld_row<DT>(a, x, row * hidden + col);
+        ld_row<DT>(b, dy, row * hidden + col);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            s[i] = fmaf(b[i], a[i] * f.pre * f.r, s[i]);
     }
-    part[chunk * hidden + col] = s;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        part[chunk * hidden + col + i] = s[i];
 }
 
-template <int DT>
+template <int DT, int N>
 __global__ void __launch_bounds__(512)
-rms_bwd_dx_kernel(const void *dy, const void *x, const void *w, void *dx, const RowStat *stat,
+rms_bwd_dx_kernel(const char *dy, const char *x, const char *w, char *dx, const RowStat *stat,
                   int64_t rows, int64_t hidden, float bias)
 {
-    using E = Elem<DT>;
     pdl_begin();
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int64_t base = row * hidden;
-        const RowStat f = stat[row];
-        for (int64_t j = threadIdx.x; j < hidden; j += blockDim.x) {
-            const float v = fmaf(E::widen1(dy, base + j), E::widen1(w, j) + bias,
-                                 -(E::widen1(x, base + j) * f.pre * f.r * f.m));
-            E::store1(dx, base + j, v * f.r * f.pre);
-        }
-    }
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+        row_dx<DT, N>(dy, x, w, dx, row * hidden, hidden, bias, stat[row]);
 }
 
-int64_t generic_chunks(int64_t rows, int64_t hidden, int sm_count)
+// Chunks of rows whose columns are summed apart (n columns a thread).
+int64_t generic_chunks(int64_t rows, int64_t hidden, int sm_count, int n)
 {
-    const int64_t col_blocks = (hidden + 255) / 256;
+    const int64_t col_blocks = (hidden + 256 * n - 1) / (256 * n);
     const int64_t want = std::max<int64_t>(1, 8 * int64_t(sm_count) / col_blocks);
     return std::max<int64_t>(1, std::min(want, rows));
 }
@@ -114,24 +165,28 @@ size_t stat_bytes(int64_t rows)
     return (static_cast<size_t>(rows) * sizeof(RowStat) + 15) / 16 * 16;
 }
 
-template <int DT> cudaError_t launch_generic(const RmsBwdArgs &a)
+template <int DT, int N> cudaError_t launch_generic(const RmsBwdArgs &a)
 {
     RowStat *stat = static_cast<RowStat *>(a.ws);
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + stat_bytes(a.rows));
+    const char *dy = static_cast<const char *>(a.dy), *x = static_cast<const char *>(a.x);
+    const char *w = static_cast<const char *>(a.w);
+    char *dx = static_cast<char *>(a.dx);
     const int grid = static_cast<int>(std::min<int64_t>(a.rows, 1 << 30));
-    cudaError_t err = launch_kernel(rms_bwd_stats_kernel<DT>, grid, 512, 0, a.base, a.dy, a.x, a.w,
-                                    stat, a.rows, a.hidden, a.bias, a.eps);
+    const bool with_dx = dx != dy && dx != x;
+    cudaError_t err = launch_kernel(rms_bwd_stats_kernel<DT, N>, grid, 512, 0, a.base, dy, x, w, dx,
+                                    stat, a.rows, a.hidden, a.bias, a.eps, with_dx);
     if (err == cudaSuccess && a.dw) {
-        const int64_t chunks = generic_chunks(a.rows, a.hidden, a.sm_count);
-        const int64_t col_blocks = (a.hidden + 255) / 256;
-        err = launch_kernel(rms_bwd_columns_kernel<DT>, static_cast<int>(chunks * col_blocks), 256,
-                            0, a.base, a.dy, a.x, stat, part, a.rows, a.hidden, col_blocks,
+        const int64_t chunks = generic_chunks(a.rows, a.hidden, a.sm_count, N);
+        const int64_t col_blocks = (a.hidden + 256 * N - 1) / (256 * N);
+        err = launch_kernel(rms_bwd_columns_kernel<DT, N>, static_cast<int>(chunks * col_blocks),
+                            256, 0, a.base, dy, x, stat, part, a.rows, a.hidden, col_blocks,
                             static_cast<int>(chunks));
         if (err == cudaSuccess)
             err = launch_colsum({part, a.dw, chunks, a.hidden, a.hidden}, {}, a.base);
     }
-    if (err == cudaSuccess)
-        err = launch_kernel(rms_bwd_dx_kernel<DT>, grid, 512, 0, a.base, a.dy, a.x, a.w, a.dx, stat,
+    if (err == cudaSuccess && !with_dx)
+        err = launch_kernel(rms_bwd_dx_kernel<DT, N>, grid, 512, 0, a.base, dy, x, w, dx, stat,
                             a.rows, a.hidden, a.bias);
     return err;
 }
@@ -154,7 +209,8 @@ template <int DT> cudaError_t launch_generic(const RmsBwdArgs &a)
 // with them kept and 84.7 us (floor 75.3) without.  Capped to 112 registers for a
 // third block of six warps: 34.6 us for 32.9 us (9001 x 2880 f16, floor 23.3).
 // Rows that are no whole vectors: 9001 x 2882 45.5 us with 4-byte vectors, 73.0 us
-// element by element, 183.8 us in three passes.
+// element by element (9001 x 2880 in the three passes above: 183.8 us).  Short
+// rows of single elements: 34351 x 331 33.9 us with eight a thread, 46.5 with 16.
 
 // Ring stages: as many as leave an SM its blocks (f32 vectors hold half as
 // many values, so a row's take twice the room).
@@ -177,7 +233,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     constexpr int NV = EPT / N;
     constexpr int S = kRowStages<DT, EPT, VB>;
     constexpr int kAhead = S > 1 ? S - 1 : 1;
-    constexpr bool kKeep = KEEP || !VEC;
+    constexpr bool kKeep = KEEP;
+    static_assert(KEEP || VEC, "single elements are always kept");
     extern __shared__ __align__(16) char ring[];
     __shared__ float2 sums[2][16];
     pdl_begin();
@@ -591,15 +648,18 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
             return launch_rows<DT, 16, 16, true>(a);
         if (a.hidden <= kMostRow)
             return launch_rows<DT, 32, 16, false>(a);
-        return launch_generic<DT>(a);
+        return launch_generic<DT, 16 / es>(a);
     }
-    if (a.hidden > 512 * 16)
-        return launch_generic<DT>(a);
-    if constexpr (es == 2)
-        if (fits(4))
-            return a.hidden <= 512 ? launch_rows<DT, 4, 4, true>(a)
-                                   : launch_rows<DT, 16, 4, true>(a);
-    return a.hidden <= 512 ? launch_rows<DT, 4, 0, true>(a) : launch_rows<DT, 16, 0, true>(a);
+    if constexpr (es == 2) {
+        if (a.hidden <= 512 * 16 && fits(4))
+            return a.hidden <= 32 * 4   ? launch_rows<DT, 4, 4, true>(a)
+                   : a.hidden <= 32 * 8 ? launch_rows<DT, 8, 4, true>(a)
+                                        : launch_rows<DT, 16, 4, true>(a);
+    }
+    return a.hidden <= 32 * 4     ? launch_rows<DT, 4, 0, true>(a)
+           : a.hidden <= 32 * 8   ? launch_rows<DT, 8, 0, true>(a)
+           : a.hidden <= 512 * 16 ? launch_rows<DT, 16, 0, true>(a)
+                                  : launch_generic<DT, 1>(a);
 }
 
 } // namespace
@@ -610,14 +670,15 @@ size_t rms_bwd_workspace(int64_t rows, int64_t hidden, int, int sm_count)
 {
     const size_t row = static_cast<size_t>(hidden) * sizeof(float);
     size_t blocks = 0;
-    for (int ept : {4, 16, 32})
-        if (hidden <= 512 * ept)
+    for (int ept : {4, 8, 16, 32})
+        if (hidden <= 512 * ept && hidden <= kMostRow)
             blocks = std::max(blocks, static_cast<size_t>(row_blocks(row_groups(hidden, ept))) *
                                           sm_count);
     if (hidden <= kHeadRow)
         blocks = std::max(blocks, static_cast<size_t>(rope_bwd_max_blocks(sm_count)));
     blocks = std::min(blocks, static_cast<size_t>(rows));
-    const size_t passes = stat_bytes(rows) + generic_chunks(rows, hidden, sm_count) * row;
+    const size_t passes = stat_bytes(rows) + std::max(generic_chunks(rows, hidden, sm_count, 1),
+                                                              generic_chunks(rows, hidden, sm_count, 8)) * row;
     return hidden <= 512 * 16 ? blocks * row : std::max(blocks * row, passes);
 }
 

@@ -56,7 +56,10 @@ struct Parts {
 // slower), 48 for two (64: 2 % slower, 40: 19 % slower).  Blocks of four warps (of
 // eight, whose places wait for the slowest: 53.3 us; appending 67.0 for 65.1).
 constexpr int kFwdWarps = 4; // of a block
-template <int DT, int VB, int TPR, int NP, int U, bool APPEND, int MODE>
+//
+// BY_TOKEN: each lane group takes a token of its own and U of its heads, for
+// tensors of so few heads that a warp within one token would stand half empty.
+template <int DT, int VB, int TPR, int NP, int U, bool APPEND, int MODE, bool BY_TOKEN>
 __global__ void __launch_bounds__(kFwdWarps * 32, NP == 4 ? 2 : NP == 2 ? 4 : U == 2 ? 10 : 8)
 rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
 {
@@ -68,26 +71,29 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     const int t = threadIdx.x % TPR;
     const int g = (threadIdx.x & 31) / TPR;
     const uint32_t item = __shfl_sync(0xFFFFFFFFu, blockIdx.x * kFwdWarps + (threadIdx.x >> 5), 0);
-    const uint32_t tok32 = item / parts.all;
-    uint32_t part = item - tok32 * parts.all;
-    const int64_t tok = tok32;
-    if (tok >= a.tokens)
+    constexpr int HS = BY_TOKEN ? 1 : G; // heads between a lane's
+    const uint32_t unit = item / parts.all; // a token, or G tokens
+    uint32_t part = item - unit * parts.all;
+    const int64_t tok = BY_TOKEN ? static_cast<int64_t>(unit) * G + g : unit;
+    if (static_cast<int64_t>(unit) * (BY_TOKEN ? G : 1) >= a.tokens)
         return; // the whole warp
+    bool ok = !BY_TOKEN || tok < a.tokens; // this lane's token is there, and good
     const bool isq = part < parts.q;
     const bool isv = APPEND && part >= parts.q + parts.k;
     part -= isq ? 0 : isv ? parts.q + parts.k : parts.q;
     const int heads = isq ? a.q_heads : a.k_heads;
-    const int h0 = static_cast<int>(part) * (U * G); // this warp's first head
+    const int h0 = static_cast<int>(part) * (U * HS); // this warp's first head
+    const int own = BY_TOKEN ? 0 : g;                 // this lane's first, behind it
     const int slots = a.head_dim / (2 * N), half_v = a.rope.rd / (2 * N);
     constexpr bool inter = MODE == kInterleaved;
 
-    const int64_t pos = a.rope.rd ? a.rope.pos[tok] : 0;
-    const int64_t slot = APPEND ? a.slots[tok] : 0;
+    const int64_t pos = a.rope.rd && ok ? a.rope.pos[tok] : 0;
+    const int64_t slot = APPEND && ok ? a.slots[tok] : 0;
 
     const char *src = isq ? a.q.p : isv ? a.v.p : a.k.p;
     const int64_t sts = isq ? a.q.ts : isv ? a.v.ts : a.k.ts;
     const int64_t shs = isq ? a.q.hs : isv ? a.v.hs : a.k.hs;
-    src += (tok * sts + (h0 + g) * shs) * E::kSize;
+    src += (tok * sts + (h0 + own) * shs) * E::kSize;
     int va[NP], vb[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j)
@@ -97,7 +103,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-            if (h0 + u * G + g < heads && t + j * TPR < slots) {
+            if (ok && h0 + u * HS + own < heads && t + j * TPR < slots) {
                 ld_head(x[u][j][0], src + va[j] * VB);
                 ld_head(x[u][j][1], src + vb[j] * VB);
             } else {
@@ -105,14 +111,17 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
                 vzero(x[u][j][1]);
             }
         }
-        src += G * shs * E::kSize;
+        src += HS * shs * E::kSize;
     }
-    if (APPEND && slot < 0)
-        return; // padding
-    if ((a.rope.rd && (pos < 0 || pos >= a.rope.max_pos)) || (APPEND && slot >= a.num_slots)) {
-        if ((threadIdx.x & 31) == 0)
+    {
+        const bool pad = APPEND && slot < 0;
+        const bool bad = (a.rope.rd && (pos < 0 || pos >= a.rope.max_pos)) ||
+                         (APPEND && slot >= a.num_slots);
+        if (ok && !pad && bad && t == 0)
             record_bad_index(a.base.status);
-        return;
+        ok = ok && !pad && !bad;
+        if (BY_TOKEN ? !__any_sync(0xFFFFFFFFu, ok) : !ok)
+            return; // the whole warp
     }
     const bool cached = APPEND && !isq;
     const bool code = cached && a.e4m3;
@@ -126,7 +135,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             r[u] = 1.f;
-            if (!norm || h0 + u * G >= heads)
+            if (!norm || h0 + u * HS >= heads)
                 continue; // the whole warp
             float sum = 0.f;
 #pragma unroll
@@ -171,8 +180,9 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
             if (p >= slots)
                 continue;
             // Whether each vector is rotated, and its angles.
-            const bool on_a = MODE == kHalvesFull || (inter ? va[j] * N < a.rope.rd : p < half_v);
-            const bool on_b = inter ? vb[j] * N < a.rope.rd : on_a;
+            const bool on_a = (!BY_TOKEN || ok) && (MODE == kHalvesFull ||
+                                                    (inter ? va[j] * N < a.rope.rd : p < half_v));
+            const bool on_b = inter ? (!BY_TOKEN || ok) && vb[j] * N < a.rope.rd : on_a;
             const float *ca = cs + (inter ? va[j] * (N / 2) : p * N), *cb = cs + vb[j] * (N / 2);
 #pragma unroll
             for (int e = 0; e < N; e += C) {
@@ -207,7 +217,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (h0 + u * G >= heads)
+                    if (h0 + u * HS >= heads)
                         continue; // the whole warp
                     float fa[C], fb[C];
                     Two A[C / 2], B[C / 2];
@@ -243,7 +253,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     // Out: in place of x, to the output tensor, or to the slot in the cache.
     char *dst;
     int64_t dhs;
-    const int64_t h = h0 + g;
+    const int64_t h = h0 + own;
     if (cached) {
         const int64_t page = slot / a.page_size;
         dhs = a.cache_hs * (code ? 1 : E::kSize);
@@ -258,7 +268,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
     for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-            if (h0 + u * G + g >= heads || t + j * TPR >= slots)
+            if (!ok || h0 + u * HS + own >= heads || t + j * TPR >= slots)
                 continue;
             if (code) {
                 st_e4m3<N>(dst + va[j] * N, x[u][j][0]);
@@ -268,7 +278,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, Parts parts)
                 st_head(dst + vb[j] * VB, x[u][j][1]);
             }
         }
-        dst += G * dhs;
+        dst += HS * dhs;
     }
 }
 
@@ -278,7 +288,7 @@ constexpr int kMostSlots = 128; // 32 lanes with four slots each
 bool takes_vectors(const RopeArgs &a, int64_t es, int64_t vb)
 {
     const int64_t n = vb / es;
-    if (!multiple(a.head_dim, 2 * n) || !multiple(a.rope.rd, 2 * n) ||
+    if (!multiple(a.head_dim, 2 * n) || !multiple(a.rope.rd, a.rope.interleaved ? n : 2 * n) ||
         a.head_dim / (2 * n) > kMostSlots ||
         !aligned(a.rope.cs, std::min<int64_t>(16, 4 * n)) || !aligned(a.qw, vb) ||
         !aligned(a.kw, vb))
@@ -293,15 +303,16 @@ bool takes_vectors(const RopeArgs &a, int64_t es, int64_t vb)
            multiple(a.slot_stride * ces, to) && multiple(a.cache_hs * ces, to);
 }
 
-template <int DT, int VB, int TPR, int NP, int U, bool APPEND, int MODE>
+template <int DT, int VB, int TPR, int NP, int U, bool APPEND, int MODE, bool BY_TOKEN = false>
 cudaError_t launch_vec(const RopeArgs &a)
 {
-    constexpr int per = U * (32 / TPR); // heads a warp takes
+    constexpr int G = 32 / TPR, per = BY_TOKEN ? U : U * G; // heads of a token a warp takes
     const uint32_t q = (a.q_heads + per - 1) / per, k = (a.k_heads + per - 1) / per;
     const Parts parts = {q, k, q + k * (APPEND ? 2 : 1)};
-    const int64_t blocks = (a.tokens * parts.all + kFwdWarps - 1) / kFwdWarps;
-    return launch_kernel(rope_kernel<DT, VB, TPR, NP, U, APPEND, MODE>, static_cast<int>(blocks),
-                         kFwdWarps * 32, 0, a.base, a, parts);
+    const int64_t units = BY_TOKEN ? (a.tokens + G - 1) / G : a.tokens;
+    const int64_t blocks = (units * parts.all + kFwdWarps - 1) / kFwdWarps;
+    return launch_kernel(rope_kernel<DT, VB, TPR, NP, U, APPEND, MODE, BY_TOKEN>,
+                         static_cast<int>(blocks), kFwdWarps * 32, 0, a.base, a, parts);
 }
 
 // Heads a lane takes.  One, while that leaves fewer than 20 warps an SM: short
@@ -309,8 +320,12 @@ cudaError_t launch_vec(const RopeArgs &a)
 // with four 4.1).  Four, when they make three full waves of 32 warps an SM and
 // leave few places in a tensor's last warp empty: 16384 tokens 52.9 us, with two
 // 54.6; but 2048 tokens 10.2 us, with two 9.6, and 16 + 16 heads of 64, half of
-// whose places would be empty, 28.2 us, with two 24.6.
-template <int DT, int TPR, bool APPEND, int MODE> cudaError_t launch_heads(const RopeArgs &a)
+// whose places would be empty, 28.2 us, with two 24.6.  Tensors of so few heads that a
+// third of the places would be empty even with two: a token a lane group (appending
+// 15274 tokens of 1 + 1 heads of 192: 25.4 -> 14.4 us; 9361 of 6 + 2 of 80: 17.8 -> 10.4).
+// The same for vectors of 8 and 4 bytes (5226 tokens of 128 + 16 heads of 80, 20
+// elements rotated: 97.8 us; with one head a lane 197).
+template <int DT, int VB, int TPR, bool APPEND, int MODE> cudaError_t launch_heads(const RopeArgs &a)
 {
     const int64_t tensors = APPEND ? 2 : 1;
     auto places = [&](int64_t per) { // heads with each tensor's last warp filled up
@@ -318,11 +333,14 @@ template <int DT, int TPR, bool APPEND, int MODE> cudaError_t launch_heads(const
     };
     constexpr int G = 32 / TPR;
     if (a.tokens * places(G) / G < 20 * a.sm_count)
-        return launch_vec<DT, 16, TPR, 1, 1, APPEND, MODE>(a);
+        return launch_vec<DT, VB, TPR, 1, 1, APPEND, MODE>(a);
+    if constexpr (VB == 16 && G > 1)
+        if (2 * places(2 * G) >= 3 * (a.q_heads + tensors * a.k_heads))
+            return launch_vec<DT, VB, TPR, 1, 2, APPEND, MODE, true>(a);
     if (4 * places(4 * G) <= 5 * places(2 * G) &&
         a.tokens * places(4 * G) / (4 * G) >= 3 * 32 * a.sm_count)
-        return launch_vec<DT, 16, TPR, 1, 4, APPEND, MODE>(a);
-    return launch_vec<DT, 16, TPR, 1, 2, APPEND, MODE>(a);
+        return launch_vec<DT, VB, TPR, 1, 4, APPEND, MODE>(a);
+    return launch_vec<DT, VB, TPR, 1, 2, APPEND, MODE>(a);
 }
 
 // The lanes of a head: the fewest that hold its slots, one each, else 32 with
@@ -332,16 +350,18 @@ template <int DT, int VB, bool APPEND, int MODE> cudaError_t launch_lanes(const 
     const int slots = a.head_dim / (2 * kVpe<DT, VB>);
     if constexpr (VB == 16) {
         if (slots <= 4)
-            return launch_heads<DT, 4, APPEND, MODE>(a);
+            return launch_heads<DT, VB, 4, APPEND, MODE>(a);
         if (slots <= 8)
-            return launch_heads<DT, 8, APPEND, MODE>(a);
-        if (slots <= 16)
-            return launch_heads<DT, 16, APPEND, MODE>(a);
-    } else if (slots <= 16) {
-        return launch_vec<DT, VB, 16, 1, 1, APPEND, MODE>(a);
+            return launch_heads<DT, VB, 8, APPEND, MODE>(a);
     }
-    if (slots <= 32)
-        return launch_vec<DT, VB, 32, 1, 1, APPEND, MODE>(a);
+    if (slots <= 16)
+        return launch_heads<DT, VB, 16, APPEND, MODE>(a);
+    if (slots <= 32) {
+        if constexpr (VB == 16)
+            return launch_vec<DT, VB, 32, 1, 1, APPEND, MODE>(a);
+        else
+            return launch_heads<DT, VB, 32, APPEND, MODE>(a);
+    }
     if constexpr (VB < 16 || Elem<DT>::kSize == 4)
         if (slots > 64)
             return launch_vec<DT, VB, 32, 4, 1, APPEND, MODE>(a);

@@ -55,7 +55,7 @@ def check(dy, x, w, bias, eps, dx, dw):
 SHAPES = [(1, 1), (3, 1), (5, 2), (1, 7), (64, 64), (17, 72), (129, 128), (33, 100), (40, 257),
           (509, 1024), (200, 1000), (77, 2048), (31, 2880), (100, 4096), (3, 4096), (26, 5120),
           (15, 7168), (9, 8192), (21, 8200), (11, 16384), (7, 20000), (4, 32768), (2, 65536),
-          (3, 100001), (2500, 96), (1200, 640), (4001, 1024), (1, 4096), (2, 300000)]
+          (3, 100001), (2500, 96), (700, 255), (700, 331), (9, 9001), (8, 15495), (600, 202), (1200, 640), (4001, 1024), (1, 4096), (2, 300000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])

@@ -67,6 +67,14 @@ SHAPES = [
     (4, 2, 1, 1024, 1024, "plain"),        # the largest head
     (300, 8, 1, 64, 34, "wide"),           # halves that straddle vectors
     (777, 40, 8, 128, 128, "wide"),
+    (150, 8, 4, 80, 20, "wide"),           # a small part rotated: 4-byte vectors for halves
+    (700, 24, 12, 96, 24, "plain"),        # 8-byte vectors, several heads a lane
+    (40, 6, 3, 80, 40, "by_head"),
+    (2000, 12, 4, 80, 20, "plain"),
+    (13001, 1, 1, 64, 64, "wide"),         # few heads: lane groups with tokens of their own
+    (5003, 3, 1, 128, 64, "by_head"),
+    (4001, 2, 2, 256, 256, "plain"),
+    (9999, 6, 2, 80, 80, "head_major"),
 ]
 
 
@@ -386,6 +394,9 @@ APPEND = [
     (23, 4, 2, 128, 128, "shifted", 16, "slots"),
     (11, 2, 2, 512, 128, "plain", 8, "slots"),
     (700, 40, 8, 128, 128, "wide", 16, "slots"),
+    (9001, 1, 1, 64, 32, "wide", 16, "heads"),     # lane groups with tokens of their own
+    (4003, 3, 1, 128, 128, "by_head", 17, "pair"),
+    (5001, 4, 2, 80, 80, "plain", 64, "split"),
 ]
 
 
@@ -517,6 +528,37 @@ def test_append_slots_outside_the_cache():
             assert torch.equal(at(kc)[s], at(k0)[s]) and torch.equal(at(vc)[s], at(v0)[s])
         good = [t for t in range(30) if t not in (4, 5, 6, 7)]
         assert torch.equal(at(vc)[slots[good]], c["v"][good].flatten(1))
+
+
+def test_bad_and_padded_tokens_between_good_ones():
+    """Few heads and many tokens: neighbouring lane groups hold good, padded and
+    bad tokens."""
+    T = 8000
+    c, g = make("bf16", T, 2, 1, 64, 64, "plain", 29, context=64)
+    kind = torch.arange(T, device="cuda") % 5           # 1: padding, 2: bad slot, 3: bad position
+    slots = torch.randperm(T + 64, generator=g, device="cuda")[:T]
+    slots[kind == 1], slots[kind == 2] = -5, T + 64
+    c["pos"][kind == 3] = 64
+    c["pos"][kind == 1] = 1 << 40
+    kc, vc = make_cache(g, "bf16", "same", (T + 64) // 16, 16, 1, 64, "slots")
+    k0, v0 = kc.clone(), vc.clone()
+    fill = R.rand(g, c["q"].shape, torch.bfloat16)
+    qo = fill.clone()
+    rn.qk_norm_rope_append(c["q"], c["k"], c["v"], c["qw"], c["kw"], c["cs"], c["pos"], slots, kc,
+                           vc, 1e-6, q_out=qo)
+    assert rn.rmsnorm_get_device_status() == rn.ERR_BAD_INDEX
+    good = (kind == 0) | (kind == 4)
+    rows = c["cs"][c["pos"][good]]
+    ref, mag = R.heads(c["q"][good], c["qw"], 0.0, 1e-6, rows, False)
+    R.assert_close(qo[good], ref, mag, K_FWD)
+    assert torch.equal(qo[~good], fill[~good])
+    at = lambda t: t.view(T + 64, 1, 64)
+    ref, mag = R.heads(c["k"][good], c["kw"], 0.0, 1e-6, rows, False)
+    R.assert_close(at(kc)[slots[good]], ref, mag, K_FWD)
+    assert torch.equal(at(vc)[slots[good]], c["v"][good])
+    rest = torch.ones(T + 64, dtype=torch.bool, device="cuda")
+    rest[slots[good]] = False
+    assert torch.equal(at(kc)[rest], at(k0)[rest]) and torch.equal(at(vc)[rest], at(v0)[rest])
 
 
 # ------------------------------------------------------------------ large offsets
