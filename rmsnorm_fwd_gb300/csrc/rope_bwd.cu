@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(256) rope_bwd_scalar_kernel(const RopeBwdArgs 
 // without the packed instructions 122 us (81 M).  128 registers and 16 warps an SM
 // (96 and 20: 114 us, spills); 3 stages (4: 92.9 us: the larger ring leaves L1 no
 // room for the angles).
-
-template <int DT, int VB, int TPR, int NP, int MODE>
+//
+// BY_TOKEN: each lane group takes a token of its own and goes through its heads,
+// for tensors of so few heads that a warp within one token would stand half empty.
+template <int DT, int VB, int TPR, int NP, int MODE, bool BY_TOKEN>
 __global__ void __launch_bounds__(kBwdThreads, NP == 1 ? kBwdBlocksPerSm : 1)
 rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
 {
@@ -169,7 +171,13 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
     const int t = lane % TPR, g = lane / TPR;
     const bool isq = static_cast<int>(blockIdx.x) < split.q;
     const int heads = isq ? a.q_heads : a.k_heads;
-    const uint32_t steps = (heads + G - 1) / G; // of a token
+    // A unit is a token, or G of them; its steps go through the heads.
+    constexpr int HS = BY_TOKEN ? 1 : G; // heads between a lane's
+    const uint32_t steps = (heads + HS - 1) / HS;
+    const int own = BY_TOKEN ? 0 : g;    // this lane's first head
+    auto token = [&](uint32_t unit) -> int64_t {
+        return BY_TOKEN ? static_cast<int64_t>(unit) * G + g : unit;
+    };
     const int slots = a.head_dim / (2 * N), half_v = a.rope.rd / (2 * N);
     const char *xb = isq ? a.q.p : a.k.p, *yb = isq ? a.qdy.p : a.kdy.p;
     char *ob = isq ? a.dq.p : a.dk.p;
@@ -187,7 +195,8 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
     // This warp's steps: an even share of the tensor's, in order.
     uint32_t left, first;
     {
-        const uint64_t all = static_cast<uint64_t>(a.tokens) * steps;
+        const uint64_t all =
+            static_cast<uint64_t>(BY_TOKEN ? (a.tokens + G - 1) / G : a.tokens) * steps;
         const uint64_t block = isq ? blockIdx.x : blockIdx.x - split.q;
         const uint64_t warps = static_cast<uint64_t>(isq ? split.q : split.k) * kWarps;
         const uint64_t i = block * kWarps + __shfl_sync(0xFFFFFFFFu, warp, 0);
@@ -226,15 +235,15 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
     const uint32_t my = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
                         warp * (S * kStage) + lane * VB;
     // The step asked for next, and the step worked on.
-    uint32_t tok_in = first / steps, in = first - tok_in * steps, left_in = left;
-    uint32_t tok = tok_in, step = in;
-    const char *px = xb + tok_in * xts + (int64_t(in) * G + g) * xhs;
-    const char *py = yb + tok_in * yts + (int64_t(in) * G + g) * yhs;
-    char *po = ob + tok * ots + (int64_t(step) * G + g) * ohs;
+    uint32_t unit_in = first / steps, in = first - unit_in * steps, left_in = left;
+    uint32_t unit = unit_in, step = in;
+    const char *px = xb + token(unit_in) * xts + (int64_t(in) * HS + own) * xhs;
+    const char *py = yb + token(unit_in) * yts + (int64_t(in) * HS + own) * yhs;
+    char *po = ob + token(unit) * ots + (int64_t(step) * HS + own) * ohs;
     // Asks a step's vectors into a stage (its two vectors of x, then of dy).
     auto ask_next = [&](uint32_t stage) {
         if (left_in) {
-            if (static_cast<int>(in) * G + g < heads) {
+            if (BY_TOKEN ? token(unit_in) < a.tokens : static_cast<int>(in) * G + g < heads) {
 #pragma unroll
                 for (int j = 0; j < NP; ++j) {
                     if (t + j * TPR >= slots)
@@ -247,13 +256,13 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
                 }
             }
             --left_in;
-            px += G * xhs;
-            py += G * yhs;
+            px += HS * xhs;
+            py += HS * yhs;
             if (++in == steps) {
                 in = 0;
-                ++tok_in;
-                px = xb + tok_in * xts + g * xhs;
-                py = yb + tok_in * yts + g * yhs;
+                ++unit_in;
+                px = xb + token(unit_in) * xts + own * xhs;
+                py = yb + token(unit_in) * yts + own * yhs;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -265,15 +274,19 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
     bool fresh = true, bad = false;
     // The token's angles as the couples take them.
     Two cc[NP][N / 2], ss[NP][N / 2];
-    int64_t next_pos = a.rope.rd && left ? a.rope.pos[tok] : 0;
+    auto position = [&](uint32_t u) -> int64_t {
+        return a.rope.rd && token(u) < a.tokens ? a.rope.pos[token(u)] : 0;
+    };
+    int64_t next_pos = left ? position(unit) : 0;
     for (; left; --left) {
         if (fresh) {
             const int64_t pos = next_pos;
             bad = a.rope.rd && (pos < 0 || pos >= a.rope.max_pos);
-            if (bad && lane == 0)
+            const bool there = !BY_TOKEN || token(unit) < a.tokens;
+            if (bad && there && t == 0)
                 record_bad_index(a.base.status);
-            if (a.rope.rd && tok + 1 < a.tokens)
-                next_pos = a.rope.pos[tok + 1];
+            bad = bad || !there;
+            next_pos = position(unit + 1);
             const float *cs = a.rope.cs + (bad ? 0 : pos) * a.rope.rd;
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -298,7 +311,7 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
         }
         // All but the newest kAhead - 1 of this lane's groups have arrived.
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        const bool live = static_cast<int>(step) * G + g < heads;
+        const bool live = BY_TOKEN ? !bad : static_cast<int>(step) * G + g < heads;
         Vec<VB> x[NP][2], y[NP][2];
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
@@ -318,7 +331,7 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
         if constexpr (S > 1) // into the stage of the step before, whose values are used
             ask_next(stage == 0 ? S - 1 : stage - 1);
         stage = stage + 1 == S ? 0 : stage + 1;
-        if (!bad) {
+        if (BY_TOKEN || !bad) { // else the whole warp's token
             // du, and the two sums of a head: x^2 and du g x.
             Two dA[NP][N / 2], dB[NP][N / 2], xA[NP][N / 2], xB[NP][N / 2];
             Two dotA = two(0.f, 0.f), dotB = dotA;
@@ -425,12 +438,12 @@ rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a, BlockSplit split)
         }
         if constexpr (S == 1)
             ask_next(0);
-        po += G * ohs;
+        po += HS * ohs;
         fresh = ++step == steps;
         if (fresh) {
             step = 0;
-            ++tok;
-            po = ob + tok * ots + g * ohs;
+            ++unit;
+            po = ob + token(unit) * ots + own * ohs;
         }
     }
     if (!a.part)
@@ -480,7 +493,7 @@ constexpr int kMostSlots = 128;
 bool takes_vectors(const RopeBwdArgs &a, int64_t es, int64_t vb)
 {
     const int64_t n = vb / es;
-    if (!multiple(a.head_dim, 2 * n) || !multiple(a.rope.rd, 2 * n) ||
+    if (!multiple(a.head_dim, 2 * n) || !multiple(a.rope.rd, a.rope.interleaved ? n : 2 * n) ||
         a.head_dim / (2 * n) > kMostSlots ||
         !aligned(a.rope.cs, std::min<int64_t>(16, 4 * n)) || !aligned(a.qw, vb) ||
         !aligned(a.kw, vb))
@@ -491,20 +504,35 @@ bool takes_vectors(const RopeBwdArgs &a, int64_t es, int64_t vb)
     return true;
 }
 
-template <int DT, int VB, int TPR, int NP, int MODE>
+template <int DT, int VB, int TPR, int NP, int MODE, bool BY_TOKEN = false>
 cudaError_t launch_vec(const RopeBwdArgs &a, BlockSplit *split)
 {
-    constexpr int G = 32 / TPR, kWarps = kBwdThreads / 32;
+    constexpr int G = 32 / TPR, HS = BY_TOKEN ? 1 : G, kWarps = kBwdThreads / 32;
     const int64_t most = rope_bwd_max_blocks(a.sm_count) - 2; // blocks on all SMs
-    const int64_t qs = (a.q_heads + G - 1) / G, ks = (a.k_heads + G - 1) / G;
+    const int64_t units = BY_TOKEN ? (a.tokens + G - 1) / G : a.tokens;
+    const int64_t qs = (a.q_heads + HS - 1) / HS, ks = (a.k_heads + HS - 1) / HS;
     auto blocks = [&](int64_t steps) { // a step a warp at least
-        const int64_t want = (a.tokens * steps + kWarps - 1) / kWarps;
+        const int64_t want = (units * steps + kWarps - 1) / kWarps;
         const int64_t share = (most * steps + (qs + ks) / 2) / (qs + ks);
         return steps ? static_cast<int>(std::max<int64_t>(1, std::min(want, share))) : 0;
     };
     *split = {blocks(qs), blocks(ks)};
-    return launch_kernel(rope_bwd_kernel<DT, VB, TPR, NP, MODE>, split->q + split->k, kBwdThreads,
-                         0, a.base, a, *split);
+    return launch_kernel(rope_bwd_kernel<DT, VB, TPR, NP, MODE, BY_TOKEN>, split->q + split->k,
+                         kBwdThreads, 0, a.base, a, *split);
+}
+
+// By tokens, where a third of the lanes would have no head (bf16, by heads and by
+// tokens: 14875 tokens of 3 + 1 heads of 80 21.8 and 15.2 us; 16384 of 1 + 1 of 128
+// 22.6 and 11.0, of 4 + 1 of 128 25.3 and 20.3, of 12 + 4 of 64 33.4 and 23.5; but
+// 32 + 8 of 128, where no lane is idle, 86.8 by heads, whose warp shares the angles).
+template <int DT, int TPR, int MODE>
+cudaError_t launch_groups(const RopeBwdArgs &a, BlockSplit *split)
+{
+    constexpr int G = 32 / TPR;
+    const int64_t qs = (a.q_heads + G - 1) / G, ks = (a.k_heads + G - 1) / G;
+    if (2 * G * (qs + ks) >= 3 * (int64_t(a.q_heads) + a.k_heads) && a.tokens >= G)
+        return launch_vec<DT, 16, TPR, 1, MODE, true>(a, split);
+    return launch_vec<DT, 16, TPR, 1, MODE>(a, split);
 }
 
 template <int DT, int VB, int MODE> cudaError_t launch_lanes(const RopeBwdArgs &a, BlockSplit *split)
@@ -512,12 +540,14 @@ template <int DT, int VB, int MODE> cudaError_t launch_lanes(const RopeBwdArgs &
     const int slots = a.head_dim / (2 * kVpe<DT, VB>);
     if constexpr (VB == 16) {
         if (slots <= 4)
-            return launch_vec<DT, VB, 4, 1, MODE>(a, split);
+            return launch_groups<DT, 4, MODE>(a, split);
         if (slots <= 8)
-            return launch_vec<DT, VB, 8, 1, MODE>(a, split);
-    }
-    if (slots <= 16)
+            return launch_groups<DT, 8, MODE>(a, split);
+        if (slots <= 16)
+            return launch_groups<DT, 16, MODE>(a, split);
+    } else if (slots <= 16) {
         return launch_vec<DT, VB, 16, 1, MODE>(a, split);
+    }
     if (slots <= 32)
         return launch_vec<DT, VB, 32, 1, MODE>(a, split);
     if constexpr (VB < 16 || Elem<DT>::kSize == 4)

@@ -561,6 +561,26 @@ def test_bad_and_padded_tokens_between_good_ones():
     assert torch.equal(at(kc)[rest], at(k0)[rest]) and torch.equal(at(vc)[rest], at(v0)[rest])
 
 
+@pytest.mark.parametrize("T,D", [(8003, 64), (3, 64), (4, 64), (5001, 128), (4001, 192)])
+def test_gradient_with_bad_tokens_between_good_ones(T, D):
+    """Few heads: neighbouring lane groups hold good and bad tokens, over the inputs."""
+    c, g = make("bf16", T, 2, 1, D, D, "plain", 31, context=64)
+    ok = torch.arange(T, device="cuda") % 3 != 1
+    c["pos"][~ok] = 64
+    c["q"][~ok], c["k"][~ok] = float("nan"), float("inf")
+    dy_q, dy_k = R.rand(g, (T, 2, D), torch.bfloat16), R.rand(g, (T, 1, D), torch.bfloat16)
+    q, k = c["q"].clone(), c["k"].clone()
+    dq, dk, dqw, dkw = rn.qk_norm_rope_backward(dy_q, dy_k, q, k, c["qw"], c["kw"], c["cs"],
+                                                c["pos"], 1e-6, dq=q, dk=k)
+    assert rn.rmsnorm_get_device_status() == rn.ERR_BAD_INDEX
+    assert dq.isnan()[~ok].all() and torch.equal(dk[~ok], c["k"][~ok])
+    rows = c["cs"][c["pos"][ok]]
+    for dx, dw, dy, x, w in ((dq, dqw, dy_q, c["q"], c["qw"]), (dk, dkw, dy_k, c["k"], c["kw"])):
+        ref = R.heads_bwd(dy[ok], x[ok], w, 0.0, 1e-6, rows, False)
+        R.assert_close(dx[ok], ref[0], ref[1], K_DX, "dx")
+        R.assert_close(dw, ref[2], ref[3], 128 + T * x.shape[1] / 1000, "dw")
+
+
 # ------------------------------------------------------------------ large offsets
 
 def test_offsets_beyond_32_bits():
