@@ -199,6 +199,11 @@ template <int DT, int N> cudaError_t launch_generic(const RmsBwdArgs &a)
 // meet in shared memory; dx = r (dy g - x r m), m = r sum(dy g x) / hidden.
 //   VB = 16 or 4: vectors of so many bytes; each thread copies its own ahead into
 //        a ring in shared memory (cp.async; only its own copies are waited for).
+//   SHIFT: rows that are no whole 16-byte vectors, in tensors that begin on a
+//        boundary.  Rows a multiple of N apart lie alike between the boundaries, so a
+//        block takes such rows alone and a thread's columns stay its own; what a
+//        row's first and last vector hold of its neighbours is taken as zeros (it
+//        may change meanwhile, where dx overwrites) and not written.
 //   VB = 0: single elements, for any row length and alignment.
 //
 // Memory bounds it.  Measured with launch_colsum (16384 x 4096 bf16, 403 MB, floor
@@ -208,21 +213,35 @@ template <int DT, int N> cudaError_t launch_generic(const RmsBwdArgs &a)
 // 16384 x 5120, where ten warps of 120 registers leave room for one block, 103 us
 // with them kept and 84.7 us (floor 75.3) without.  Capped to 112 registers for a
 // third block of six warps: 34.6 us for 32.9 us (9001 x 2880 f16, floor 23.3).
-// Rows that are no whole vectors: 9001 x 2882 45.5 us with 4-byte vectors, 73.0 us
-// element by element (9001 x 2880 in the three passes above: 183.8 us).  Short
-// rows of single elements: 34351 x 331 33.9 us with eight a thread, 46.5 with 16.
+// Rows that are no whole vectors, shifted: 9001 x 2881 39.5 us, element by element
+// 73.1; 9001 x 2882 39.6 us, with 4-byte vectors 45.4; 4000 x 12001 75.7 us, in the
+// three passes above 208.  The edges cost 7 us of the 39.5 (9001 x 2880: 32.6).
 
 // Ring stages: as many as leave an SM its blocks (f32 vectors hold half as
 // many values, so a row's take twice the room).
 template <int DT, int EPT, int VB>
 constexpr int kRowStages = VB == 0 ? 0 : Elem<DT>::kSize == 2 ? 3 : EPT <= 16 ? 2 : 1;
 
+// The first `bytes` of 16, the others as zeros.
+__device__ inline void cp_async_part(uint32_t to, const char *from, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+
+template <int N> __device__ inline void zero_first(float (&f)[N], int n)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = i < n ? 0.f : f[i];
+}
+
 struct RowGroups {
     int warps;  // of a group
     int groups; // of a block
 };
 
-template <int DT, int EPT, int VB, bool KEEP>
+template <int DT, int EPT, int VB, bool KEEP, bool SHIFT>
 __global__ void __launch_bounds__(512, 1)
 rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, float *part,
                     int64_t rows, int32_t hidden, float bias, float eps, RowGroups rg)
@@ -243,8 +262,12 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     const int group = threadIdx.x / threads, t = threadIdx.x - group * threads;
     const int warp = t >> 5;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * rg.groups;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rg.groups + group;
-    const int nvec = hidden / N;
+    const int64_t row0 = SHIFT ? blockIdx.x + static_cast<int64_t>(gridDim.x) * group
+                               : static_cast<int64_t>(blockIdx.x) * rg.groups + group;
+    // SHIFT: elements between a vector's boundary and the row, the same for all
+    // rows of the block; column c lies at place c + shift of the vectors.
+    const int shift = SHIFT ? static_cast<int>(blockIdx.x * static_cast<uint64_t>(hidden) % N) : 0;
+    const int end = hidden + shift, nvec = SHIFT ? (end + N - 1) / N : hidden / N;
     const int64_t row_bytes = static_cast<int64_t>(hidden) * E::kSize;
     const float inv_n = 1.f / static_cast<float>(hidden);
 
@@ -292,8 +315,17 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
         if constexpr (VEC) {
             Vec<VB> u;
             vzero(u);
-            if (v < nvec)
+            if constexpr (SHIFT) {
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int c = v * N + i - shift;
+                    f[i] = c >= 0 && c < hidden ? E::widen1(w, c) : 0.f;
+                }
+                put<DT, VB, N>(u, 0, f);
+            } else if (v < nvec) {
                 ld_const(u, w + v * VB);
+            }
             if constexpr (kKeep) {
                 float f[N];
                 get<DT, VB, N>(f, u, 0);
@@ -313,14 +345,21 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     auto ask_next = [&](int stage) {
         if constexpr (VEC) {
             if (next < rows) {
-                const char *px = x + next * row_bytes, *py = dy + next * row_bytes;
+                const int64_t at = next * row_bytes - shift * E::kSize;
+                const char *px = x + at, *py = dy + at;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int v = t + j * threads;
                     if (v < nvec) {
                         const uint32_t p = my + (stage * 2 * NV + 2 * j) * step;
-                        cp_async<VB>(p, px + v * VB);
-                        cp_async<VB>(p + step, py + v * VB);
+                        if constexpr (SHIFT) { // nothing behind the row's end
+                            const int bytes = min(VB, (end - v * N) * E::kSize);
+                            cp_async_part(p, px + v * VB, bytes);
+                            cp_async_part(p + step, py + v * VB, bytes);
+                        } else {
+                            cp_async<VB>(p, px + v * VB);
+                            cp_async<VB>(p + step, py + v * VB);
+                        }
                     }
                 }
             }
@@ -332,6 +371,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     for (int s = 0; s < kAhead; ++s)
         ask_next(s);
     int stage = 0;
+    // Of this thread's first vector, the elements of the row before: taken as zeros.
+    const int before = SHIFT && t == 0 ? shift : 0;
     for (int64_t row = row0; row < rows; row += stride) {
         const uint32_t here = my + stage * 2 * NV * step;
         Two x2[kKeep ? EPT / 2 : 1], y2[kKeep ? EPT / 2 : 1];
@@ -365,6 +406,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                     if (in)
                         ld_ring(v, here + 2 * j * step);
                     get<DT, VB, N>(f, v, 0);
+                    if (SHIFT && j == 0)
+                        zero_first<N>(f, before);
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i)
                         xv[i] = two(f[2 * i], f[2 * i + 1]);
@@ -372,6 +415,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                     if (in)
                         ld_ring(v, here + (2 * j + 1) * step);
                     get<DT, VB, N>(f, v, 0);
+                    if (SHIFT && j == 0)
+                        zero_first<N>(f, before);
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i)
                         yv[i] = two(f[2 * i], f[2 * i + 1]);
@@ -467,10 +512,20 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                     f[i] *= k;
             }
             if constexpr (VEC) {
-                Vec<VB> o;
-                put<DT, VB, N>(o, 0, f);
-                if (t + j * threads < nvec)
-                    st_head(po + (t + j * threads) * VB, o);
+                const int v = t + j * threads;
+                if (!SHIFT || (v * N >= shift && v * N + N <= end)) {
+                    Vec<VB> o;
+                    put<DT, VB, N>(o, 0, f);
+                    if (SHIFT || v < nvec)
+                        st_head(po - shift * E::kSize + v * VB, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int c = v * N + i - shift;
+                        if (c >= 0 && c < hidden)
+                            E::store1(po, c, f[i]);
+                    }
+                }
             } else {
                 const int c0 = t + 2 * j * threads, c1 = c0 + threads;
                 if (c0 < hidden)
@@ -509,7 +564,7 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                 buf[i * threads] = v;
                 continue;
             }
-            if constexpr (N >= 4) {
+            if constexpr (N >= 4 && !SHIFT) {
                 const int c = (t + i * 4 / N * threads) * N + i * 4 % N;
                 if (c < hidden)
                     *reinterpret_cast<float4 *>(out + c) = v;
@@ -517,8 +572,8 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                 const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int c = (t + (4 * i + e) / N * threads) * N + e % N;
-                    if (c < hidden)
+                    const int c = (t + (4 * i + e) / N * threads) * N + (4 * i + e) % N - shift;
+                    if (c >= 0 && c < hidden)
                         out[c] = f[e];
                 }
             }
@@ -577,24 +632,33 @@ cudaError_t row_occupancy(const void *kernel, int threads, int smem, int *blocks
     return cudaSuccess;
 }
 
-template <int DT, int EPT, int VB, bool KEEP> cudaError_t launch_rows(const RmsBwdArgs &a)
+// Vectors of n elements that a row may take when it starts anywhere in the first.
+int64_t shifted_vectors(int64_t hidden, int n) { return (hidden + 2 * n - 2) / n; }
+
+template <int DT, int EPT, int VB, bool KEEP, bool SHIFT = false>
+cudaError_t launch_rows(const RmsBwdArgs &a)
 {
     constexpr int N = VB ? VB / Elem<DT>::kSize : 1;
     constexpr int NV = EPT / N, S = kRowStages<DT, EPT, VB>;
-    const RowGroups rg = row_groups(a.hidden / N, NV);
+    const RowGroups rg = row_groups(SHIFT ? shifted_vectors(a.hidden, N) : a.hidden / N, NV);
     const int threads = rg.warps * rg.groups * 32;
     // The ring (and g), and the sums of dw over the groups.
     const int smem = std::max((S * 2 + (KEEP ? 0 : 1)) * NV * VB * threads,
                               rg.groups > 1 ? rg.warps * 32 * EPT * 4 : 0);
-    auto *kernel = rms_bwd_rows_kernel<DT, EPT, VB, KEEP>;
+    auto *kernel = rms_bwd_rows_kernel<DT, EPT, VB, KEEP, SHIFT>;
     int blocks_per_sm = 0;
     cudaError_t err = row_occupancy(reinterpret_cast<const void *>(kernel), threads, smem,
                                     &blocks_per_sm);
     if (err != cudaSuccess)
         return err;
     const int64_t want = (a.rows + rg.groups - 1) / rg.groups;
-    const int grid = static_cast<int>(std::min<int64_t>(
-        want, int64_t(std::min(blocks_per_sm, row_blocks(rg))) * a.sm_count));
+    const int64_t most = int64_t(std::min(blocks_per_sm, row_blocks(rg))) * a.sm_count;
+    int64_t blocks = std::min(want, most);
+    if (SHIFT) { // rows a grid apart start alike
+        blocks = (blocks + N - 1) / N * N;
+        blocks = std::min(blocks <= most ? blocks : blocks - N, a.rows);
+    }
+    const int grid = static_cast<int>(blocks);
     float *part = a.dw ? static_cast<float *>(a.ws) : nullptr;
     err = launch_kernel(kernel, grid, threads, smem, a.base, static_cast<const char *>(a.dy),
                         static_cast<const char *>(a.x), static_cast<const char *>(a.w),
@@ -650,6 +714,18 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
             return launch_rows<DT, 32, 16, false>(a);
         return launch_generic<DT, 16 / es>(a);
     }
+    // Vectors over the rows' boundaries, beyond rows of 128 (65536 rows of 129: 26.5 us,
+    // 41.3 by single elements; of 65: 25.9 us and 17.8).
+    if (a.hidden > 32 * 4 && aligned(a.dy, 16) && aligned(a.x, 16) && aligned(a.dx, 16) &&
+        a.sm_count >= 16 / es) {
+        const int64_t places = shifted_vectors(a.hidden, 16 / es) * (16 / es);
+        if (places <= 32 * 8)
+            return launch_rows<DT, 8, 16, true, true>(a);
+        if (places <= 512 * 16) // ten warps a row too: 16384 x 5001 122 us, not kept 136
+            return launch_rows<DT, 16, 16, true, true>(a);
+        if (places <= kMostRow)
+            return launch_rows<DT, 32, 16, false, true>(a);
+    }
     if constexpr (es == 2) {
         if (a.hidden <= 512 * 16 && fits(4))
             return a.hidden <= 32 * 4   ? launch_rows<DT, 4, 4, true>(a)
@@ -672,8 +748,10 @@ size_t rms_bwd_workspace(int64_t rows, int64_t hidden, int, int sm_count)
     size_t blocks = 0;
     for (int ept : {4, 8, 16, 32})
         if (hidden <= 512 * ept && hidden <= kMostRow)
-            blocks = std::max(blocks, static_cast<size_t>(row_blocks(row_groups(hidden, ept))) *
-                                          sm_count);
+            for (int n : {1, 4, 8}) // single elements or whole vectors, or shifted vectors
+                if (ept >= n)
+                    blocks = std::max(blocks, static_cast<size_t>(row_blocks(row_groups(
+                                                  shifted_vectors(hidden, n), ept / n))) * sm_count);
     if (hidden <= kHeadRow)
         blocks = std::max(blocks, static_cast<size_t>(rope_bwd_max_blocks(sm_count)));
     blocks = std::min(blocks, static_cast<size_t>(rows));

@@ -55,7 +55,10 @@ def check(dy, x, w, bias, eps, dx, dw):
 SHAPES = [(1, 1), (3, 1), (5, 2), (1, 7), (64, 64), (17, 72), (129, 128), (33, 100), (40, 257),
           (509, 1024), (200, 1000), (77, 2048), (31, 2880), (100, 4096), (3, 4096), (26, 5120),
           (15, 7168), (9, 8192), (21, 8200), (11, 16384), (7, 20000), (4, 32768), (2, 65536),
-          (3, 100001), (2500, 96), (700, 255), (700, 331), (9, 9001), (8, 15495), (600, 202), (1200, 640), (4001, 1024), (1, 4096), (2, 300000)]
+          (3, 100001), (2500, 96), (700, 255), (700, 331), (9, 9001), (8, 15495), (600, 202), (1200, 640), (4001, 1024),
+          (1, 4096), (2, 300000), (1219, 1003), (3001, 247), (2001, 249), (5000, 33), (2000, 1026),
+          (610, 4067), (305, 5113), (310, 8177), (160, 8179), (7, 8191), (170, 16369), (160, 16371),
+          (154, 16383)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
@@ -85,6 +88,27 @@ def test_gradient(rows, hidden, dtype):
 def test_unaligned_tensors(rows, hidden, dtype):
     dy, x, w, _ = make(dtype, rows, hidden, 2, shift=1)
     check(dy, x, w, 0.0, 1e-6, *rn.rms_norm_backward(dy, x, w, 1e-6, 0.0))
+
+
+@pytest.mark.parametrize("rows,hidden", [(3000, 331), (2000, 1026), (1500, 4067), (400, 12289)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_between_vector_boundaries_keep_to_themselves(dtype, rows, hidden):
+    """Rows that share vectors with their neighbours, every other one of NaN, and what lies
+    behind the last."""
+    dt = R.DT[dtype]
+    dy, x, w, g = make(dtype, rows, hidden, 8)
+    x[1::2], dy[1::2] = float("nan"), float("inf")
+    room = torch.full((rows * hidden + 64,), 7.0, dtype=dt, device="cuda")
+    dx = room[:rows * hidden].view(rows, hidden)
+    rn.rms_norm_backward(dy, x, w, 1e-6, 0.0, dx=dx)
+    assert (room[rows * hidden:] == 7).all() and dx[1::2].isnan().all()
+    good = dy[::2].contiguous(), x[::2].contiguous()
+    _, dw = rn.rms_norm_backward(*good, w, 1e-6, 0.0)
+    check(*good, w, 0.0, 1e-6, dx[::2], dw)
+    for over in (x.clone(), dy.clone()):
+        a, b = (dy, over) if over[1, 0].isnan() else (over, x)
+        rn.rms_norm_backward(a, b, w, 1e-6, 0.0, dx=over, weight_grad=False)
+        assert torch.equal(over[::2], dx[::2])
 
 
 @pytest.mark.parametrize("rows,hidden", [(16384, 1024), (5000, 4096), (30000, 72)])
