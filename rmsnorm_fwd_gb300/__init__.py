@@ -726,7 +726,7 @@ def _heads(t, name: str, dtype, device) -> tuple[bytes, int]:
             if n != 1:
                 if tokens == 1:
                     step = s
-                elif s != step * tokens:
+                elif s != step * tokens and t.numel():
                     raise ValueError(f"the leading dimensions of {name} must step evenly")
                 tokens *= n
     else:

@@ -290,6 +290,19 @@ def test_gradient_without_tokens_or_keys():
     assert dk is None and not dkw.any()
 
 
+@pytest.mark.parametrize("lead", [(0,), (2, 0), (0, 2), (3, 0, 2)])
+def test_empty_batches(lead):
+    e, w = torch.empty(*lead, 4, 64, device="cuda"), torch.ones(64, device="cuda")
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    cs = R.table(4, 64)
+    assert rn.qk_norm_rope(e, e, w, w, cs, none, 1e-6)[0] is e
+    dq, dk, dqw, _ = rn.qk_norm_rope_backward(e, e, e, e, w, w, cs, none, 1e-6)
+    assert dq.shape == e.shape == dk.shape and not dqw.any()
+    kc, vc = torch.zeros(2, 1, 16, 4, 64, device="cuda")
+    assert rn.qk_norm_rope_append(e, e, e, w, w, cs, none, none, kc, vc, 1e-6) is e
+    assert not kc.any() and not vc.any()
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_gradient_against_differences(inter):
     """<dx, a> + <dw, b> against the central difference of <dy, y> in 64 bits
