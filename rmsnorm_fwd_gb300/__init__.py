@@ -712,7 +712,10 @@ def _heads(t, name: str, dtype, device) -> tuple[bytes, int]:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.dtype is not dtype or t.device != device:
         raise TypeError(f"{name} must have the dtype and device of the other tensors")
-    shape, strides = t.shape, t.stride()
+    shape = t.shape
+    if len(shape) == 3 and t.is_contiguous():
+        return _HEADS.pack(t.data_ptr(), 0, 0), shape[0]
+    strides = t.stride()
     if len(shape) == 3:
         tokens, heads, dim = shape
         step, head_step, last = strides
@@ -845,8 +848,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
         raise ValueError("q must be a CUDA tensor (there is no CPU path)")
     device, dtype = q.device, q.dtype
     qh, tokens = _heads(q, "q", dtype, device)
-    q_shape = q.shape
-    q_heads, head_dim = q_shape[-2:]
+    q_heads, head_dim = q.shape[-2:]
     if not _here(device, stream):
         with _there(device, stream, dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions,
                     dq, dk):
@@ -865,13 +867,13 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, pos
         _same_shape(dk_out, k, "dk_out")
         ky = _heads(dk_out, "dk_out", dtype, device)[0]
         if dk is None:
-            dk = torch.empty(k.shape, dtype=dtype, device=device)
+            dk = torch.empty_like(k, memory_format=torch.contiguous_format)
             kd = _HEADS.pack(dk.data_ptr(), 0, 0)
         else:
             _same_shape(dk, k, "dk")
             kd = _heads(dk, "dk", dtype, device)[0]
     if dq is None:
-        dq = torch.empty(q_shape, dtype=dtype, device=device)
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
         qd = _HEADS.pack(dq.data_ptr(), 0, 0)
     else:
         _same_shape(dq, q, "dq")
