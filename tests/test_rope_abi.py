@@ -266,6 +266,7 @@ def test_tensor_refusals():
 class Fake:
     """A tensor's layout, as the checks read it."""
     is_cuda, dtype, device = True, "t", "cuda:0"
+    dense = False  # what is_contiguous answers; the strides are read where it is false
 
     def __init__(self, shape, strides):
         self.shape, self._s = tuple(shape), tuple(strides)
@@ -278,6 +279,9 @@ class Fake:
         for s in self.shape:
             n *= s
         return n
+
+    def is_contiguous(self):
+        return self.dense
 
     def data_ptr(self):
         return P
@@ -317,6 +321,11 @@ def test_layouts_of_tensors():
     assert (h.token_stride, h.head_stride, n) == (0, 0, 1)
     h, n = of((0, 8, 64), (512, 64, 1))
     assert n == 0
+    t = Fake((5, 8, 64), (512, 64, 1))
+    t.dense = True
+    packed, n = rn._heads(t, "q", Fake.dtype, Fake.device)
+    h = rn.Heads.from_buffer_copy(packed)
+    assert (h.data, h.token_stride, h.head_stride, n) == (P, 0, 0, 5)  # the default strides
     for shape, strides in (((64,), (1,)), ((8, 64), (64, 1)), ((5, 8, 64), (512, 64, 2)),
                            ((2, 5, 8, 64), (4501, 900, 64, 1)), ((5, 8, 64), (0, 64, 1)),
                            ((5, 8, 64), (512, 0, 1)), ((3, 5, 8, 64), (0, 512, 64, 1))):
