@@ -213,9 +213,9 @@ template <int DT, int N> cudaError_t launch_generic(const RmsBwdArgs &a)
 // 16384 x 5120, where ten warps of 120 registers leave room for one block, 103 us
 // with them kept and 84.7 us (floor 75.3) without.  Capped to 112 registers for a
 // third block of six warps: 34.6 us for 32.9 us (9001 x 2880 f16, floor 23.3).
-// Rows that are no whole vectors, shifted: 9001 x 2881 39.5 us, element by element
-// 73.1; 9001 x 2882 39.6 us, with 4-byte vectors 45.4; 4000 x 12001 75.7 us, in the
-// three passes above 208.  The edges cost 7 us of the 39.5 (9001 x 2880: 32.6).
+// Rows that are no whole vectors, shifted: 9001 x 2881 40.1 us, element by element
+// 73.1; 9001 x 2882 40.3 us, with 4-byte vectors 45.4; 4000 x 12001 71.1 us, in the
+// three passes above 208.  The edges cost 7 us of the 40 (9001 x 2880: 32.9).
 
 // Ring stages: as many as leave an SM its blocks (f32 vectors hold half as
 // many values, so a row's take twice the room).
@@ -547,7 +547,7 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
     float *out = part + static_cast<int64_t>(blockIdx.x) * hidden;
     float4 *buf = reinterpret_cast<float4 *>(ring) + t; // [EPT / 4][threads]
     for (int q = 0; q < rg.groups; ++q) {
-        if (rg.groups > 1)
+        if (SHIFT || rg.groups > 1)
             __syncthreads();
         if (group != q)
             continue;
@@ -560,11 +560,11 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                 const float4 o = buf[i * threads];
                 v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
             }
-            if (q < rg.groups - 1) {
+            if (SHIFT || q < rg.groups - 1) {
                 buf[i * threads] = v;
                 continue;
             }
-            if constexpr (N >= 4 && !SHIFT) {
+            if constexpr (N >= 4) {
                 const int c = (t + i * 4 / N * threads) * N + i * 4 % N;
                 if (c < hidden)
                     *reinterpret_cast<float4 *>(out + c) = v;
@@ -572,10 +572,24 @@ rms_bwd_rows_kernel(const char *dy, const char *x, const char *w, char *dx, floa
                 const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int c = (t + (4 * i + e) / N * threads) * N + (4 * i + e) % N - shift;
-                    if (c >= 0 && c < hidden)
+                    const int c = (t + (4 * i + e) / N * threads) * N + e % N;
+                    if (c < hidden)
                         out[c] = f[e];
                 }
+            }
+        }
+    }
+    if constexpr (SHIFT) {
+        // From there in order of columns: a thread's own lie N floats apart, and with
+        // single stores so far apart 419 x 15495 took 27.5 us for 23.9.
+        __syncthreads();
+        const float *all = reinterpret_cast<const float *>(ring);
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) {
+            for (int i = threadIdx.x; i < threads * N; i += blockDim.x) {
+                const int c = j * threads * N + i - shift, e = i % N;
+                if (c >= 0 && c < hidden)
+                    out[c] = all[((j * N + e) / 4 * threads + i / N) * 4 + e % 4];
             }
         }
     }
@@ -644,7 +658,7 @@ cudaError_t launch_rows(const RmsBwdArgs &a)
     const int threads = rg.warps * rg.groups * 32;
     // The ring (and g), and the sums of dw over the groups.
     const int smem = std::max((S * 2 + (KEEP ? 0 : 1)) * NV * VB * threads,
-                              rg.groups > 1 ? rg.warps * 32 * EPT * 4 : 0);
+                              SHIFT || rg.groups > 1 ? rg.warps * 32 * EPT * 4 : 0);
     auto *kernel = rms_bwd_rows_kernel<DT, EPT, VB, KEEP, SHIFT>;
     int blocks_per_sm = 0;
     cudaError_t err = row_occupancy(reinterpret_cast<const void *>(kernel), threads, smem,
