@@ -718,7 +718,16 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
         h.sm_count = a.sm_count;
         return launch_rope_bwd(h, DT);
     }
+    // Many rows that two warps would half fill: one warp a row (bf16 27063 x 576 24.6 us,
+    // with two 29.0; 22130 x 723 29.1 us, with two 32.9; but 3151 x 723 11.6 us, with two
+    // 10.3, and f32 22130 x 723 41.2 us, with two 37.7).
+    [[maybe_unused]] auto one_warp = [&](int64_t n) {
+        return n > 512 && n <= 24 * 32 && a.rows >= 64 * int64_t(a.sm_count);
+    };
     if (fits(16)) {
+        if constexpr (es == 2)
+            if (one_warp(a.hidden))
+                return launch_rows<DT, 24, 16, false>(a);
         // Ten warps a row: a second block on an SM fits without x and dy kept.
         if (a.hidden > 9 * 512 && a.hidden <= 10 * 512)
             return launch_rows<DT, 16, 16, false>(a);
@@ -735,6 +744,9 @@ template <int DT> cudaError_t launch(const RmsBwdArgs &a)
         const int64_t places = shifted_vectors(a.hidden, 16 / es) * (16 / es);
         if (places <= 32 * 8)
             return launch_rows<DT, 8, 16, true, true>(a);
+        if constexpr (es == 2)
+            if (one_warp(places))
+                return launch_rows<DT, 24, 16, false, true>(a);
         if (places <= 512 * 16) // ten warps a row too: 16384 x 5001 122 us, not kept 136
             return launch_rows<DT, 16, 16, true, true>(a);
         if (places <= kMostRow)
@@ -760,7 +772,7 @@ size_t rms_bwd_workspace(int64_t rows, int64_t hidden, int, int sm_count)
 {
     const size_t row = static_cast<size_t>(hidden) * sizeof(float);
     size_t blocks = 0;
-    for (int ept : {4, 8, 16, 32})
+    for (int ept : {4, 8, 16, 24, 32})
         if (hidden <= 512 * ept && hidden <= kMostRow)
             for (int n : {1, 4, 8}) // single elements or whole vectors, or shifted vectors
                 if (ept >= n)

@@ -58,7 +58,7 @@ SHAPES = [(1, 1), (3, 1), (5, 2), (1, 7), (64, 64), (17, 72), (129, 128), (33, 1
           (3, 100001), (2500, 96), (700, 255), (700, 331), (9, 9001), (8, 15495), (600, 202), (1200, 640), (4001, 1024),
           (1, 4096), (2, 300000), (1219, 1003), (3001, 247), (2001, 249), (5000, 33), (2000, 1026),
           (610, 4067), (305, 5113), (310, 8177), (160, 8179), (7, 8191), (170, 16369), (160, 16371),
-          (154, 16383)]
+          (154, 16383), (12001, 576), (11000, 723), (10003, 768), (10003, 755)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
